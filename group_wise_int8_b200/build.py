@@ -24,8 +24,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libwino_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libwino_b200_debug.so")
 SOURCES = ["plan.cpp", "api.cu", "weight_transform.cu", "input_transform.cu", "hadamard_tc.cu",
-           "hadamard_simt.cu", "output_transform.cu", "input_quant.cu", "noalloc.cu", "fused_small.cu"]
-HEADERS = ["plan.h", "common.cuh", "sm100.cuh", "kernels.h"]
+           "hadamard_simt.cu", "output_transform.cu", "input_quant.cu", "noalloc.cu", "fused_small.cu",
+           "ops_api.cu", "group_norm.cu", "matmul_simt.cu"]
+HEADERS = ["plan.h", "common.cuh", "sm100.cuh", "kernels.h", "ops.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -15,6 +15,7 @@
 
 #include "../../include/wino.h"
 #include "kernels.h"
+#include "ops.h"
 #include "plan.h"
 
 struct wino_plan_s {
@@ -922,6 +923,6 @@ int wino_profile_end(wino_plan_t p, float* ms, int max_launches, int* launches_p
     return rc;
 }
 
-int wino_last_cuda_error(wino_plan_t p) { return p ? p->last_cuda : 0; }
+int wino_last_cuda_error(wino_plan_t p) { return p ? p->last_cuda : ops_last_cuda_error(); }
 
 }  // extern "C"

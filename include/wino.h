@@ -345,8 +345,99 @@ int wino_profile_begin(wino_plan_t plan, int max_calls);
 int wino_profile_end(wino_plan_t plan, float* ms_per_launch, int max_launches, int* launches_per_call,
                      int* calls);
 
-/* Last CUDA error code seen by this plan (cudaError_t as int), 0 if none. */
+/* Last CUDA error code seen by this plan (cudaError_t as int), 0 if none.  plan == NULL: the last
+ * one of the calling thread's calls that take no plan (wino_group_norm, wino_matmul and their
+ * error query). */
 int wino_last_cuda_error(wino_plan_t plan);
+
+/* ------------------------------------------- operators beside the convolution
+ * The two operators that a residual network runs between its convolutions, on
+ * the same NHWC activations.  They need no plan and no workspace, launch one
+ * kernel on `stream` and return (asynchronous; capturable in a CUDA graph).  The
+ * current device must be the stream's, and every pointer must be of that
+ * device.  Results repeat bit for bit.  Pointers need their element type's
+ * alignment only; 16-byte aligned bases and pitches (in bytes) run fastest.
+ * A pitch is the distance in elements between consecutive pixels (rows); it is
+ * at least the row's length, so a tensor may be a channel range of a wider one.
+ * An output may not share memory with an input, but for the in-place forms
+ * named below (WINO_ERR_INVALID_ARG).  (The paper has no counterpart.) */
+#define WINO_ACT_NONE 0
+#define WINO_ACT_SILU 1 /* v / (1 + exp(-v)) */
+#define WINO_ACT_GELU 2 /* v * Phi(v), Phi the normal distribution function (the erf form) */
+
+#define WINO_GROUP_NORM_MAX_CHANNELS 16384
+
+/*
+ * wino_group_norm -- group normalisation over NHWC pixels, then an activation:
+ *   v = [x | x2] + add,  y = act((v - mean) / sqrt(var + eps) * gamma + beta),
+ * mean and (biased) variance over the pixels of an image and the channels of a
+ * group, groups of (C + C2) / groups consecutive channels.
+ *   x      [N][H][W][C], pixel pitch x_pitch, x_dtype (WINO_BF16 or WINO_F32).
+ *   x2     [N][H][W][C2] of the same type, or NULL (C2 = 0): the channels after
+ *          x's, as if the two had been concatenated; a group may span both.
+ *   add    fp32 [N][C + C2] or NULL: added per image and channel before the
+ *          statistics (a time embedding's projection).
+ *   gamma, beta  fp32 [C + C2], or NULL for 1 and 0.
+ *   y      [N][H][W][C + C2], pixel pitch y_pitch, y_dtype; y may be x itself
+ *          (same pointer, pitch and type, no x2).
+ * Statistics are fp32 sums around a pivot, so a mean that is large against the
+ * spread costs no digits; y is rounded once (to nearest even).
+ * Errors: INVALID_ARG (sizes not positive, (C + C2) % groups != 0, pitch, type,
+ * alignment, overlap, eps negative or not finite), UNSUPPORTED (C + C2 above
+ * WINO_GROUP_NORM_MAX_CHANNELS), CUDA.
+ */
+typedef struct wino_group_norm_args {
+    const void* x;
+    const void* x2;
+    const float* add;
+    const float* gamma;
+    const float* beta;
+    void* y;
+    int64_t x_pitch, x2_pitch, y_pitch;
+    int x_dtype, y_dtype;
+    int N, H, W, C, C2, groups;
+    int act; /* WINO_ACT_* */
+    float eps;
+} wino_group_norm_args;
+int wino_group_norm(const wino_group_norm_args* args, void* stream);
+
+/*
+ * wino_matmul -- out = act([a | a2] w^T + bias) + residual: a 1x1 convolution
+ * (rows are pixels), a projection of an embedding (rows are images) or a
+ * classifier.
+ *   a        [M][K], pitch a_pitch, dtype (WINO_BF16 or WINO_F32).
+ *   a2       [M][K2] of the same type, or NULL (K2 = 0): the columns after a's.
+ *   w        [N][K + K2] of the same type, pitch w_pitch.
+ *   bias     fp32 [N] or NULL.
+ *   residual [M][N] of out_dtype, or NULL; it may be out itself (same pointer
+ *            and pitch).
+ *   out      [M][N], pitch out_pitch, out_dtype.
+ * Sums, activation and the residual's addition are fp32 (bf16 products are
+ * exact in it); out is rounded once (to nearest even).
+ * Errors: INVALID_ARG (sizes not positive, pitch, type, alignment, overlap),
+ * CUDA.
+ */
+typedef struct wino_matmul_args {
+    const void* a;
+    const void* a2;
+    const void* w;
+    const float* bias;
+    const void* residual;
+    void* out;
+    int64_t a_pitch, a2_pitch, w_pitch, residual_pitch, out_pitch;
+    int dtype, out_dtype;
+    int M, N, K, K2;
+    int act; /* WINO_ACT_* */
+    int reserved;
+} wino_matmul_args;
+int wino_matmul(const wino_matmul_args* args, void* stream);
+
+/* Synchronises stream and returns the first error that kernels of wino_group_norm and wino_matmul
+ * recorded on the current device since the last call of this function, which clears it:
+ * WINO_OK, WINO_ERR_DEVICE_TIMEOUT (a bounded wait expired, the kernel returned early and its output is
+ * undefined) or (debug build) WINO_ERR_DEVICE_BOUNDS.  One word per device and kernel family: it does not
+ * tell calls apart.  Not capturable. */
+int wino_check_device_error_ops(void* stream);
 
 /* Static description of a status code. */
 const char* wino_status_string(int status);
