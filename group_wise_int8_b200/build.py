@@ -25,7 +25,7 @@ LIB = os.path.join(HERE, "libwino_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libwino_b200_debug.so")
 SOURCES = ["plan.cpp", "api.cu", "weight_transform.cu", "input_transform.cu", "hadamard_tc.cu",
            "hadamard_simt.cu", "output_transform.cu", "input_quant.cu", "noalloc.cu", "fused_small.cu",
-           "ops_api.cu", "group_norm.cu", "matmul_simt.cu"]
+           "ops_api.cu", "group_norm.cu", "matmul_simt.cu", "matmul_tc.cu"]
 HEADERS = ["plan.h", "common.cuh", "sm100.cuh", "kernels.h", "ops.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

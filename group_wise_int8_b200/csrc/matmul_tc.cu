@@ -1,0 +1,497 @@
+// Matrix product with bias, activation and residual on the sm_100a tensor cores,
+// for outputs of many tiles: out = act([a | a2] w^T + bias) + residual in bf16
+// operands and fp32 sums.
+//
+// Bound: the tensor cores when K is long, device memory (activations in, residual
+// in, output out) for the 1x1 convolutions of an image network.
+//
+// Kernel structure (persistent; a cluster of two CTAs, one pair per two SMs, walks
+// tiles of 256 rows x BN columns, BN a multiple of 32 up to 256):
+//   The pair's MMA (tcgen05 cta_group::2, M = 256) reads A's 128 rows and half
+//   of W's BN rows from each CTA's shared memory, so that a CTA loads (128 + BN/2)
+//   rows per K step instead of 128 + BN: the L2-to-SM traffic of a lone CTA's
+//   128 x 256 tiles would exceed what the SMs' ports carry at the tensor
+//   cores' rate.
+//   warp 0    = TMA producer: 64 columns of K (128 bytes, 128-byte swizzle) of a
+//               or a2 and of w per stage; both CTAs' loads complete on the
+//               leader's barrier; columns past K read zeros.
+//   warp 1    = TMEM allocator; in the leader the MMA issuer; two accumulators of BN columns,
+//               so that the next tile's MMAs run under this tile's epilogue.
+//   warps 4-11 = epilogue, two groups of four warps (the four TMEM lane
+//               quadrants) that take the tile's 32-column chunks in turn: fp32
+//               accumulator + bias, activation, + residual, rounded once into a chunk
+//               buffer (64- or 128-byte swizzle), stored by TMA.  The residual
+//               chunk has been loaded by TMA into that same buffer, up to three
+//               chunks ahead.
+// Outputs or residuals whose base or pitch is no multiple of 16 bytes (an odd
+// number of columns) cannot go through TMA: there (DIRECT) each warp moves its own
+// 32 rows between the chunk buffer and memory, a row of 32 columns at a time.
+// Every mbarrier wait is bounded; on expiry the CTA records the error and leaves.
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ops.h"
+#include "sm100.cuh"
+
+namespace wino {
+namespace {
+
+using namespace sm100;
+
+__device__ int g_err;   // first error since matmul_tc_take_error
+
+constexpr int kThreads = 384;
+constexpr int kBK = 64;               // K per stage
+constexpr int kMaxStages = 8;
+constexpr int kChunk = 32;            // columns per epilogue chunk
+constexpr int kARows = 128;           // rows of A per CTA
+constexpr uint32_t kABytes = kARows * kBK * 2;
+constexpr size_t kSmemBudget = 226 * 1024;
+
+struct TcArgs {
+    MatmulArgs m;
+    int BN, stages, tiles_m, tiles_n, steps0, steps1;
+};
+
+template <typename TO>
+struct Chunk {
+    static constexpr int kRow = kChunk * (int)sizeof(TO);     // bytes of a row: 64 or 128, the swizzle's width
+    static constexpr int kBytes = kARows * kRow;
+    static constexpr int kBuffers = sizeof(TO) == 2 ? 4 : 2;  // per epilogue group
+    // byte offset of 16-byte unit j of a row (the TMA swizzle of that width)
+    static __device__ __forceinline__ uint32_t unit(int row, int j) {
+        return (uint32_t)(row * kRow + ((j ^ (sizeof(TO) == 2 ? (row >> 1) & 3 : row & 7)) << 4));
+    }
+    static __device__ __forceinline__ uint32_t at(int row, int col) {
+        constexpr int per = 16 / (int)sizeof(TO);
+        return unit(row, col / per) + (uint32_t)(col % per * (int)sizeof(TO));
+    }
+};
+
+struct Tail {
+    uint64_t full[kMaxStages];     // leader: both CTAs' operands of the stage have landed
+    uint64_t empty[kMaxStages];    // the pair's MMAs have read the stage
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];         // leader: both CTAs' epilogues have read the accumulator
+    uint64_t buf_full[2][4];       // a group's chunk buffer is free to use, its residual (if any) landed
+    uint64_t buf_ready[2][4];      // ... and holds the output chunk: the group's four warps have written it
+    alignas(16) float bias[8][kChunk];   // per epilogue warp
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 0;; ++it) {
+        const bool ok = mbar_try_wait(bar, parity);
+        if (__all_sync(0xffffffffu, ok)) return true;
+        if ((it & 63u) == 63u) {
+            bool stop = *abort_flag != 0;
+            if (!stop && globaltimer() - t0 > kWaitLimitNs) {
+                stop = true;
+                *abort_flag = 1;
+                atomicCAS(&g_err, 0, kDevErrTimeout);
+            }
+            if (__any_sync(0xffffffffu, stop)) return false;
+        }
+    }
+}
+
+// The chunks of one epilogue group, tile after tile: chunk c of tile t, c = g, g + 2, ...
+struct Cursor {
+    int tile, c, step, tiles, tiles_n, BN, N, g;
+    __device__ __forceinline__ int chunks() const {   // of the tile
+        const int n0 = tile % tiles_n * BN;
+        return (min(BN, N - n0) + kChunk - 1) / kChunk;
+    }
+    __device__ __forceinline__ bool valid() const { return tile < tiles; }
+    __device__ __forceinline__ void settle() {        // to the next existing chunk
+        while (tile < tiles && c >= chunks()) {
+            tile += step;
+            c = g;
+        }
+    }
+    __device__ __forceinline__ void next() {
+        c += 2;
+        settle();
+    }
+};
+
+template <typename TO, bool DIRECT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    matmul_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+                     const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
+                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes, const TcArgs p) {
+    using Ch = Chunk<TO>;
+    constexpr int NB = DIRECT ? 1 : Ch::kBuffers;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t stage_bytes = kABytes + (uint32_t)(p.BN / 2) * kBK * 2;
+    unsigned char* chunks = smem + (size_t)p.stages * stage_bytes;   // [2 groups][NB][Ch::kBytes]
+    Tail* tail = reinterpret_cast<Tail*>(chunks + 2 * NB * Ch::kBytes);
+    volatile int* abort_flag = &tail->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int tiles = p.tiles_m * p.tiles_n, step = (int)(gridDim.x / 2), first = (int)(blockIdx.x / 2);
+    const int steps = p.steps0 + p.steps1;
+    grid_dependents_launch();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            mbar_init(&tail->full[s], 1);
+            mbar_init(&tail->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tail->acc_full[b], 1);
+            mbar_init(&tail->acc_empty[b], 16);   // the epilogue warps of both CTAs
+            for (int i = 0; i < NB; ++i) {
+                mbar_init(&tail->buf_full[b][i], 1);
+                mbar_init(&tail->buf_ready[b][i], 4);
+            }
+        }
+        tail->abort_flag = 0;
+        fence_mbar_init();
+        fence_proxy_async_smem();
+        prefetch_tensormap(&tmA0);
+        prefetch_tensormap(&tmW0);
+        if (!DIRECT) prefetch_tensormap(&tmOut);
+    }
+    if (warp == 1) tmem_alloc_pair(&tail->tmem_base, 512);
+    grid_dependency_wait();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers exist before either signals the other's
+    tc_fence_after();
+    const uint32_t tmem_base = tail->tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            int st = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; ok && t < tiles; t += step) {
+                const int m0 = t / p.tiles_n * 256 + (int)rank * kARows;
+                const int n0 = t % p.tiles_n * p.BN + (int)rank * (p.BN / 2);
+                for (int s = 0; s < steps; ++s) {
+                    if (!mbar_wait(&tail->empty[st], phase ^ 1u, abort_flag, &g_err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (rank == 0) mbar_arrive_expect_tx(&tail->full[st], 2 * stage_bytes);
+                    const uint32_t bar = map_rank(&tail->full[st], 0);
+                    unsigned char* dst = smem + (size_t)st * stage_bytes;
+                    const bool second = s >= p.steps0;
+                    const int k = (second ? s - p.steps0 : s) * kBK;
+                    tma_load_2d_pair(dst, second ? &tmA1 : &tmA0, bar, k, m0);
+                    tma_load_2d_pair(dst + kABytes, second ? &tmW1 : &tmW0, bar, k, n0);
+                    if (++st == p.stages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // --------------------------------------------------------- MMA issuer
+        if (rank == 0 && lane == 0) {
+            const uint32_t idesc = idesc_bf16(256, p.BN);
+            const uint64_t a_desc = smem_desc_kmajor(smem_u32(smem), 128);
+            const uint64_t w_desc = smem_desc_kmajor(smem_u32(smem) + kABytes, 128);
+            const int last0 = (p.m.K0 - (p.steps0 - 1) * kBK + 15) / 16;                 // K-steps of 16 in a source's
+            const int last1 = p.steps1 ? (p.m.K1 - (p.steps1 - 1) * kBK + 15) / 16 : 0;  // last stage
+            int st = 0, it = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; ok && t < tiles; t += step, ++it) {
+                const int b = it & 1;
+                if (!mbar_wait(&tail->acc_empty[b], ((it >> 1) & 1) ^ 1u, abort_flag, &g_err)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + (uint32_t)b * 256u;
+                for (int s = 0; s < steps; ++s) {
+                    if (!mbar_wait(&tail->full[st], phase, abort_flag, &g_err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t off = (uint64_t)(((uint32_t)st * stage_bytes) >> 4);
+                    const int kn = s == p.steps0 - 1 ? last0 : (s == steps - 1 ? last1 : kBK / 16);
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 16; ++kk)
+                        if (kk < kn) mma_bf16_pair(d, a_desc + off + 2 * kk, w_desc + off + 2 * kk, idesc, (s | kk) != 0);
+                    mma_commit_pair(&tail->empty[st]);
+                    if (++st == p.stages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) mma_commit_pair(&tail->acc_full[b]);
+            }
+        }
+    } else if (warp >= 4) {
+        // ----------------------------------------------------------- epilogue
+        const int g = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
+        const uint32_t t_lane = tmem_base + ((uint32_t)(32 * quad) << 16);
+        unsigned char* ring = chunks + (size_t)g * NB * Ch::kBytes;
+        float* bias_s = tail->bias[warp - 4];
+        const uint32_t release = map_rank(&tail->acc_empty[0], 0);
+        const bool chief = quad == 0 && lane == 0;   // issues the group's TMA operations
+        const bool has_res = p.m.res != nullptr;
+        auto origin_m = [&](int t) { return t / p.tiles_n * 256 + (int)rank * kARows; };
+        auto origin_n = [&](int t, int c) { return t % p.tiles_n * p.BN + c * kChunk; };
+        Cursor cur{first, g, step, tiles, p.tiles_n, p.BN, p.m.N, g};
+        Cursor ahead = cur;
+        ahead.settle();
+        auto hand_out = [&](int buf) {   // a free buffer, for the chunk at `ahead`
+            if (!has_res) {
+                mbar_arrive(&tail->buf_full[g][buf]);
+            } else if (ahead.valid()) {
+                mbar_arrive_expect_tx(&tail->buf_full[g][buf], Ch::kBytes);
+                tma_load_2d(ring + buf * Ch::kBytes, &tmRes, &tail->buf_full[g][buf], origin_n(ahead.tile, ahead.c),
+                            origin_m(ahead.tile));
+                ahead.next();
+            }
+        };
+        if (!DIRECT && chief)
+            for (int i = 0; i < NB - 1; ++i) hand_out(i);
+
+        int it = 0, buf = 0;
+        uint32_t rphase = 0;
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += step, ++it) {
+            const int b = it & 1;
+            cur.tile = t;
+            const int nch = cur.chunks(), m0 = origin_m(t);
+            if (!warp_wait(&tail->acc_full[b], (uint32_t)((it >> 1) & 1), abort_flag)) break;
+            tc_fence_after();
+            for (int c = g; c < nch; c += 2) {
+                const int n0 = origin_n(t, c);
+                unsigned char* cb = ring + (size_t)buf * Ch::kBytes;
+                uint32_t r[kChunk];
+                tmem_ld<kChunk>(t_lane + (uint32_t)(b * 256 + c * kChunk), r);
+                bias_s[lane] = p.m.bias && n0 + lane < p.m.N ? p.m.bias[n0 + lane] : 0.0f;
+                if (DIRECT && has_res) {
+                    const TO* res = static_cast<const TO*>(p.m.res);
+                    const int rows = min(32, p.m.M - m0 - 32 * quad);
+                    if (n0 + lane < p.m.N)
+#pragma unroll 8
+                        for (int i = 0; i < rows; ++i)
+                            *reinterpret_cast<TO*>(cb + Ch::at(32 * quad + i, lane)) =
+                                res[(size_t)(m0 + 32 * quad + i) * p.m.ldr + n0 + lane];
+                }
+                __syncwarp();
+                tmem_ld_wait();
+                tmem_regs_ready(r);
+                if (c + 2 >= nch) {   // this warp's last read of the accumulator
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
+                }
+                float v[kChunk];
+#pragma unroll
+                for (int j = 0; j < kChunk; j += 4) {
+                    const float4 bb = *reinterpret_cast<const float4*>(bias_s + j);
+                    v[j] = __uint_as_float(r[j]) + bb.x;
+                    v[j + 1] = __uint_as_float(r[j + 1]) + bb.y;
+                    v[j + 2] = __uint_as_float(r[j + 2]) + bb.z;
+                    v[j + 3] = __uint_as_float(r[j + 3]) + bb.w;
+                }
+                if (p.m.act == WINO_ACT_SILU) {
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) v[j] = silu<sizeof(TO) == 2>(v[j]);
+                } else if (p.m.act == WINO_ACT_GELU) {
+#pragma unroll
+                    for (int j = 0; j < kChunk; ++j) v[j] = activate<sizeof(TO) == 2>(v[j], WINO_ACT_GELU);
+                }
+                if (!DIRECT && !warp_wait(&tail->buf_full[g][buf], rphase, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                if (has_res) {
+#pragma unroll
+                    for (int j = 0; j < Ch::kRow / 16; ++j) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(cb + Ch::unit(row, j));
+                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (sizeof(TO) == 2) {
+                                v[8 * j + 2 * i] += __uint_as_float(x[i] << 16);
+                                v[8 * j + 2 * i + 1] += __uint_as_float(x[i] & 0xffff0000u);
+                            } else {
+                                v[4 * j + i] += __uint_as_float(x[i]);
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < Ch::kRow / 16; ++j) {
+                    uint4 w;
+                    if constexpr (sizeof(TO) == 2) {
+                        uint32_t x[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+                            x[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        w = make_uint4(x[0], x[1], x[2], x[3]);
+                    } else {
+                        w = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                       __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+                    }
+                    *reinterpret_cast<uint4*>(cb + Ch::unit(row, j)) = w;
+                }
+                if constexpr (DIRECT) {
+                    __syncwarp();
+                    TO* out = static_cast<TO*>(p.m.out);
+                    const int rows = min(32, p.m.M - m0 - 32 * quad);
+                    const size_t limit = (size_t)(p.m.M - 1) * p.m.ldo + p.m.N;
+                    if (n0 + lane < p.m.N)
+#pragma unroll 8
+                        for (int i = 0; i < rows; ++i) {
+                            const size_t at = (size_t)(m0 + 32 * quad + i) * p.m.ldo + n0 + lane;
+                            if (in_bounds(at, limit, &g_err))
+                                out[at] = *reinterpret_cast<const TO*>(cb + Ch::at(32 * quad + i, lane));
+                        }
+                    __syncwarp();
+                } else {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tail->buf_ready[g][buf]);
+                    if (quad == 0) {
+                        if (!warp_wait(&tail->buf_ready[g][buf], rphase, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) {
+                            if (m0 < p.m.M) tma_store_2d(&tmOut, cb, n0, m0);
+                            bulk_commit();
+                            bulk_wait_read<1>();   // the store before this one has read its buffer, which is handed out again
+                            hand_out((buf + NB - 1) % NB);
+                        }
+                        __syncwarp();
+                    }
+                    if (++buf == NB) {
+                        buf = 0;
+                        rphase ^= 1u;
+                    }
+                }
+            }
+            if (g >= nch) {   // a tile of one chunk leaves the second group nothing to read
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
+            }
+        }
+        if (!DIRECT && chief) bulk_wait_read<0>();
+    }
+
+    // Every role is done: the MMAs that read either CTA's shared memory have completed (both epilogues waited
+    // for the last accumulator), and no arrival is under way to a CTA that has left.
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+size_t smem_bytes(const TcArgs& a, bool direct) {
+    const size_t chunk = a.m.out_bf16 ? Chunk<__nv_bfloat16>::kBytes : Chunk<float>::kBytes;
+    const size_t buffers = direct ? 1 : (a.m.out_bf16 ? Chunk<__nv_bfloat16>::kBuffers : Chunk<float>::kBuffers);
+    return 1024 + (size_t)a.stages * (kABytes + a.BN / 2 * kBK * 2) + 2 * buffers * chunk + sizeof(Tail);
+}
+
+bool tma_ok(const void* p, long pitch, int rows, size_t es) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows == 1 || (size_t)pitch * es % 16 == 0);
+}
+
+bool map_2d(CUtensorMap* map, bool bf16, const void* base, int cols, int rows, long pitch, int box_cols, int box_rows) {
+    const size_t es = bf16 ? 2 : 4;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(rows == 1 ? ((size_t)cols * es + 15) / 16 * 16 : (size_t)pitch * es)};
+    const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    return make_tensor_map(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims,
+                           strides, box, box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+}  // namespace
+
+bool matmul_tma_operands(const MatmulArgs& a) {
+    return a.bf16 && tma_ok(a.a, a.lda, a.M, 2) && tma_ok(a.w, a.ldw, a.N, 2) &&
+           (a.K1 == 0 || (tma_ok(a.a2, a.lda2, a.M, 2) && a.K0 % 8 == 0));
+}
+
+// Operand tensor maps: boxes of 64 columns x 128 rows of a and a2, x w_rows rows of w.
+bool matmul_operand_maps(const MatmulArgs& a, int w_rows, CUtensorMap (&map)[4]) {
+    const void* w1 = static_cast<const __nv_bfloat16*>(a.w) + a.K0;
+    if (!map_2d(&map[0], true, a.a, a.K0, a.M, a.lda, kBK, kARows) || !map_2d(&map[2], true, a.w, a.K0, a.N, a.ldw, kBK, w_rows))
+        return false;
+    if (a.K1 == 0) {
+        map[1] = map[0];
+        map[3] = map[2];
+        return true;
+    }
+    return map_2d(&map[1], true, a.a2, a.K1, a.M, a.lda2, kBK, kARows) && map_2d(&map[3], true, w1, a.K1, a.N, a.ldw, kBK, w_rows);
+}
+
+// The tile width: as few rounds of tiles over the SM pairs as possible, weighing a round by its width
+// and a fixed part (filling the pipeline and the accumulator hand-over).
+int matmul_tc_width(const MatmulArgs& a, int num_sms) {
+    const long rows = (a.M + 255L) / 256, pairs = num_sms / 2;
+    int best = 256;
+    double best_cost = 0;
+    for (int bn = 256; bn >= 64; bn -= 32) {
+        const long tiles = rows * ((a.N + (long)bn - 1) / bn);
+        const double cost = (double)((tiles + pairs - 1) / pairs) * (bn + 24);
+        if (best_cost == 0 || cost < best_cost) {
+            best_cost = cost;
+            best = bn;
+        }
+    }
+    return best;
+}
+
+cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStream_t st) {
+    TcArgs a = {};
+    a.m = m;
+    a.BN = bn > 0 ? bn : matmul_tc_width(m, num_sms);
+    const long tiles_m = (m.M + 255L) / 256, tiles_n = (m.N + (long)a.BN - 1) / a.BN;
+    if (tiles_m * tiles_n > 1073741824L) return cudaErrorInvalidConfiguration;
+    a.tiles_m = (int)tiles_m;
+    a.tiles_n = (int)tiles_n;
+    a.steps0 = (m.K0 + kBK - 1) / kBK;
+    a.steps1 = (m.K1 + kBK - 1) / kBK;
+    const size_t so = m.out_bf16 ? 2 : 4;
+    const bool direct = !tma_ok(m.out, m.ldo, m.M, so) || (m.res && !tma_ok(m.res, m.ldr, m.M, so));
+    CUtensorMap map[4], out, res;
+    if (!matmul_operand_maps(m, a.BN / 2, map)) return cudaErrorInvalidValue;
+    out = res = map[0];
+    if (!direct) {
+        if (!map_2d(&out, m.out_bf16, m.out, m.N, m.M, m.ldo, kChunk, kARows)) return cudaErrorInvalidValue;
+        if (m.res && !map_2d(&res, m.out_bf16, m.res, m.N, m.M, m.ldr, kChunk, kARows)) return cudaErrorInvalidValue;
+    }
+    a.stages = kMaxStages;
+    while (a.stages > 2 && smem_bytes(a, direct) > kSmemBudget) --a.stages;
+    const size_t smem = smem_bytes(a, direct);
+    const long pairs = std::min<long>(tiles_m * tiles_n, std::max(1, num_sms / 2));
+    static bool done[4][64];
+    auto go = [&](auto kern, bool (&d)[64]) -> cudaError_t {
+        const cudaError_t e = allow_smem(kern, kSmemBudget, d);
+        if (e != cudaSuccess) return e;
+        return launch_dependent(kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, st, map[0], map[1], map[2], map[3],
+                                out, res, a);
+    };
+    if (m.out_bf16)
+        return direct ? go(matmul_tc_kernel<__nv_bfloat16, true>, done[0]) : go(matmul_tc_kernel<__nv_bfloat16, false>, done[1]);
+    return direct ? go(matmul_tc_kernel<float, true>, done[2]) : go(matmul_tc_kernel<float, false>, done[3]);
+}
+
+cudaError_t matmul_tc_take_error(int* err) {
+    cudaError_t e = cudaMemcpyFromSymbol(err, g_err, sizeof(int));
+    const int zero = 0;
+    if (e == cudaSuccess && *err) e = cudaMemcpyToSymbol(g_err, &zero, sizeof(int));
+    return e;
+}
+
+}  // namespace wino

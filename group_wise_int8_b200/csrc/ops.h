@@ -2,6 +2,7 @@
 // normalisation with an activation on NHWC activations, and the matrix product
 // with bias, activation and residual in its epilogue.
 #pragma once
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <cstddef>
@@ -71,12 +72,21 @@ struct MatmulArgs {
     bool bf16;             // operand type: bf16 or fp32
     bool out_bf16;
 };
+// The CUDA-core kernel: any type, size, pitch and alignment.
 cudaError_t launch_matmul_simt(const MatmulArgs& a, cudaStream_t st);
+
+// The tensor-core kernels take bf16 operands that TMA can read (16-byte aligned bases and pitches).
+bool matmul_tma_operands(const MatmulArgs& a);
+bool matmul_operand_maps(const MatmulArgs& a, int w_rows, CUtensorMap (&map)[4]);   // a, a2, w for a, w for a2
+// Persistent pair kernel for outputs of many tiles; bn: tile width (a multiple of 32 up to 256), 0: by the rule.
+int matmul_tc_width(const MatmulArgs& a, int num_sms);
+cudaError_t launch_matmul_tc(const MatmulArgs& a, int bn, int num_sms, cudaStream_t st);
 
 // Device error words of the kernels above on the current device: the first error recorded since
 // the last call of the function, which clears it (0: none).
 cudaError_t group_norm_take_error(int* err);
 cudaError_t matmul_simt_take_error(int* err);
+cudaError_t matmul_tc_take_error(int* err);
 
 // Last CUDA error of the calling thread's calls without a plan.
 int ops_last_cuda_error();

@@ -163,7 +163,8 @@ int wino_matmul(const wino_matmul_args* g, void* stream) {
     a.bf16 = g->dtype == WINO_BF16;
     a.out_bf16 = g->out_dtype == WINO_BF16;
     nvtxRangePushA("wino: matmul");
-    const cudaError_t e = launch_matmul_simt(a, static_cast<cudaStream_t>(stream));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = a.M > 16 && matmul_tma_operands(a) ? launch_matmul_tc(a, 0, sms(), st) : launch_matmul_simt(a, st);
     nvtxRangePop();
     return status(e);
 }
@@ -172,7 +173,7 @@ int wino_check_device_error_ops(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return status(e);
     int first = 0;
-    for (auto take : {group_norm_take_error, matmul_simt_take_error}) {
+    for (auto take : {group_norm_take_error, matmul_simt_take_error, matmul_tc_take_error}) {
         int v = 0;
         if ((e = take(&v)) != cudaSuccess) return status(e);
         if (first == 0) first = v;
