@@ -12,7 +12,7 @@
 // thread-block cluster of up to 16 CTAs takes one (image, slab), each CTA a
 // contiguous range of pixels.  A CTA loads its part once into shared memory
 // while it accumulates statistics, the cluster exchanges one (mean, M2) pair per
-// group and CTA through distributed shared memory, and the CTA normalises from
+// group and CTA by writing it into every CTA's shared memory, and the CTA normalises from
 // shared memory.  No workspace, no atomics, one launch; the order of every
 // sum is fixed by the shape, so results repeat bit for bit.  A part that does
 // not fit is kept as far as it fits and the rest is read again (mostly from L2).
@@ -20,58 +20,114 @@
 // Statistics: a thread owns one vector of channels and strides over pixels.
 // Per channel it sums d and d*d with d = x - p, p the first value it sees, so
 // that a mean far from zero costs no digits, and (mean, M2) pairs are joined by
-//   mean = sum n_i mean_i / n,  M2 = sum M2_i + sum n_i (mean_i - mean)^2,
-// again around one of the means.  All of it is fp32.
+//   mean = sum n_i mean_i / n,  M2 = sum M2_i + sum n_i (mean_i - mean)^2:
+// a channel's pairs around one of their means, the channels of a group and the CTAs of a cluster (whose
+// means may lie far apart) with the joint mean first.  All of it is fp32; M2 never falls below zero but by rounding.
 #include <algorithm>
-#include <cooperative_groups.h>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
 #include "ops.h"
+#include "sm100.cuh"
 
 namespace wino {
 namespace {
 
 __device__ int g_err;   // first failed index check since group_norm_take_error (debug build)
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;          // two CTAs per SM, with registers for a vector's parameters
 constexpr int kMaxCluster = 16;
-constexpr int kResBytes = 56 * 1024;   // a CTA's share kept in shared memory (three CTAs per SM)
+constexpr int kMaxParams = 2048;       // channels whose parameters fit in shared memory
+constexpr int kResBytes = 90 * 1024;   // a CTA's share of the input kept in shared memory
 
+// A thread's VEC consecutive values: 16 bytes, or one value where alignment allows no more.
 template <typename T, int VEC>
-struct Vec;
-template <>
-struct Vec<__nv_bfloat16, 8> {
+struct Vec {
     using Raw = uint4;
-    static __device__ __forceinline__ void load(const Raw& r, float (&v)[8]) {
+    static __device__ __forceinline__ void load(const Raw& r, float (&v)[VEC]) {
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            if constexpr (sizeof(T) == 2) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                v[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+};
+template <typename T>
+struct Vec<T, 1> {
+    using Raw = typename std::conditional<sizeof(T) == 2, uint16_t, uint32_t>::type;
+    static __device__ __forceinline__ void load(const Raw& r, float (&v)[1]) {
+        v[0] = __uint_as_float(sizeof(T) == 2 ? (uint32_t)r << 16 : (uint32_t)r);
+    }
+};
+
+// Running sums of d and d * d, d = x - p, of VEC channels (packed pairs where VEC is even).
+template <int VEC>
+struct Sums {
+    static constexpr int kPairs = VEC / 2;
+    uint64_t p[kPairs], s[kPairs], q[kPairs];
+    __device__ __forceinline__ void start(const float (&x)[VEC]) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            p[i] = f2_pack(x[2 * i], x[2 * i + 1]);
+            s[i] = q[i] = 0ull;
+        }
+    }
+    __device__ __forceinline__ void add(const float (&x)[VEC]) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const uint64_t d = f2_sub(f2_pack(x[2 * i], x[2 * i + 1]), p[i]);
+            s[i] = f2_add(s[i], d);
+            q[i] = f2_fma(d, d, q[i]);
+        }
+    }
+    __device__ __forceinline__ void get(float (&pv)[VEC], float (&sv)[VEC], float (&qv)[VEC]) const {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            f2_unpack(p[i], pv[2 * i], pv[2 * i + 1]);
+            f2_unpack(s[i], sv[2 * i], sv[2 * i + 1]);
+            f2_unpack(q[i], qv[2 * i], qv[2 * i + 1]);
         }
     }
 };
 template <>
-struct Vec<float, 4> {
-    using Raw = uint4;
-    static __device__ __forceinline__ void load(const Raw& r, float (&v)[4]) {
-        v[0] = __uint_as_float(r.x);
-        v[1] = __uint_as_float(r.y);
-        v[2] = __uint_as_float(r.z);
-        v[3] = __uint_as_float(r.w);
+struct Sums<1> {
+    float p, s, q;
+    __device__ __forceinline__ void start(const float (&x)[1]) {
+        p = x[0];
+        s = q = 0.0f;
+    }
+    __device__ __forceinline__ void add(const float (&x)[1]) {
+        const float d = x[0] - p;
+        s += d;
+        q = fmaf(d, d, q);
+    }
+    __device__ __forceinline__ void get(float (&pv)[1], float (&sv)[1], float (&qv)[1]) const {
+        pv[0] = p;
+        sv[0] = s;
+        qv[0] = q;
     }
 };
-template <>
-struct Vec<__nv_bfloat16, 1> {
-    using Raw = uint16_t;
-    static __device__ __forceinline__ void load(const Raw& r, float (&v)[1]) { v[0] = __uint_as_float((uint32_t)r << 16); }
-};
-template <>
-struct Vec<float, 1> {
-    using Raw = uint32_t;
-    static __device__ __forceinline__ void load(const Raw& r, float (&v)[1]) { v[0] = __uint_as_float(r); }
-};
+
+// 16 bytes global -> shared without a register (counted in this thread's cp.async groups).
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_async4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -105,233 +161,378 @@ __device__ __forceinline__ void store(TO* p, const float (&v)[VEC], bool vec) {
     }
 }
 
-// Layout of a CTA's shared memory (bytes): kept rows | per-thread (mean, M2) table | per-group
-// (mean, M2) of this CTA | per-group (mean, 1/std) of the cluster.
-struct Shape {
-    int nv, RP, TV, nvp;
-    __host__ __device__ Shape(int channels, int vec) {
-        nv = channels / vec;                    // vectors per row of the slab
-        TV = nv < kThreads ? nv : kThreads;     // vectors taken at a time
-        RP = kThreads / TV;                     // rows taken at a time
-        nvp = nv | 1;                           // table pitch: odd, so that a column read has no bank conflicts
-    }
-    __host__ __device__ size_t table() const { return (size_t)RP * nvp; }   // entries per vector lane
+// What the kernel needs to know of its split, worked out once on the host.  A row offset is a thread's first row
+// within its CTA's pixels; it takes every RP-th row from there.  Index 1 of a pair: the first `extra` CTAs of a
+// cluster, which take one row more.
+struct Split {
+    int cluster, slabs, gps;      // CTAs per (image, slab); slabs per image; groups per slab
+    int nch, nv;                  // channels and vectors of a slab's row
+    int TV, RP;                   // vectors taken at a time; row offsets
+    int nvp, entries;             // table pitch (odd: no bank conflicts down a column); table entries per lane of a vector
+    uint32_t inv_tv;              // ceil(2^20 / TV): tid / TV = tid * inv_tv >> 20 for tid < 512
+    uint32_t inv_cg;              // ceil(2^32 / cg): channel / cg = umulhi(channel, inv_cg) for channel < 2^14 (0: cg = 1)
+    int cg;
+    int log_cluster, log_lanes;   // log2 of cluster and of the lanes of a warp that join one channel
+    int share, extra;             // rows per CTA
+    int res_rows, res_per;        // rows kept in shared memory when not all are (a multiple of RP); those of one offset
+    int fewer[2], more[2];        // an offset has `fewer` rows, the first `more` offsets one more
+    float inv0[2], inv1[2];       // 1 / fewer (0 when none), 1 / (fewer + 1)
+    float inv_rows[2];            // 1 / rows (0 when none)
+    float inv_cg_f, inv_all;      // 1 / cg, 1 / (HW cg)
+    int keep_bytes, prm_at, nprm; // bytes of the kept rows; where the parameters start; their channels (0: not kept)
+    bool vec_y;                   // y takes whole-vector stores
 };
 
-__device__ __forceinline__ float2 ld_cluster(const float2* p, int rank) {
-    namespace cg = cooperative_groups;
-    return *cg::this_cluster().map_shared_rank(p, rank);
+// A thread's vector of a pixel: where it starts in its source, and the source's end (in elements).
+template <typename TI>
+struct Source {
+    const TI* p;
+    long ld;
+    size_t base, limit;
+    __device__ __forceinline__ Source(const GroupNormArgs& a, long pixel, int ch) {
+        const bool second = ch >= a.C0;
+        ld = second ? a.ld1 : a.ld0;
+        base = (size_t)pixel * ld + (second ? ch - a.C0 : ch);
+        limit = (size_t)((long)a.N * a.HW - 1) * ld + (second ? a.C1 : a.C0);
+        p = static_cast<const TI*>(second ? a.x2 : a.x) + base;
+    }
+};
+
+// Stores to the same shared variable of another CTA of the cluster.
+__device__ __forceinline__ void st_cluster(float2* p, int rank, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(sm100::map_rank(p, (uint32_t)rank)), "f"(v.x), "f"(v.y)
+                 : "memory");
 }
 
-template <typename TI, typename TO, int VEC>
-__global__ void __launch_bounds__(kThreads) group_norm_kernel(const GroupNormArgs a) {
-    namespace cg = cooperative_groups;
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+template <typename TI, typename TO, int VEC, int ACT>
+__global__ void __launch_bounds__(kThreads, 2) group_norm_kernel(const GroupNormArgs a, const Split k) {
     using V = Vec<TI, VEC>;
     using Raw = typename V::Raw;
     constexpr bool FAST = sizeof(TO) == 2;
     extern __shared__ __align__(16) unsigned char smem[];
     const int C = a.C0 + a.C1;
-    const int CS = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
-    const long unit = (long)blockIdx.x / CS;
-    const int n = (int)(unit / a.slabs), slab = (int)(unit - (long)n * a.slabs);
-    const int g0 = slab * a.gps, ng = min(a.gps, a.groups - g0);
-    const int ch0 = g0 * a.cg, nch = ng * a.cg;
-    const Shape sh(nch, VEC);
-    const int nv = sh.nv, TV = sh.TV, RP = sh.RP;
-    const long row0 = a.HW * rank / CS;
-    const int rows = (int)(a.HW * (rank + 1) / CS - row0);
-    const int res = min(rows, a.res_rows);
+    const int CS = k.cluster, rank = (int)blockIdx.x & (CS - 1), slab = (int)(blockIdx.x >> k.log_cluster);
+    const int n = (int)(blockIdx.z * gridDim.y + blockIdx.y);
+    if (n >= a.N) return;   // (a whole cluster)
+    if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");   // (waited for before the exchange)
+    const int ch0 = slab * k.nch, nv = k.nv, RP = k.RP, entries = k.entries;
+    const int x = rank < k.extra ? 1 : 0;
+    const int rows = k.share + x;
+    const long row0 = (long)n * a.HW + (long)rank * k.share + min(rank, k.extra);   // first pixel, over all images
+    // (selected, not indexed: an index would put the parameters in local memory)
+    const int fewer = x ? k.fewer[1] : k.fewer[0], more = x ? k.more[1] : k.more[0];
+    const float inv0 = x ? k.inv0[1] : k.inv0[0], inv1 = x ? k.inv1[1] : k.inv1[0];
+    const float inv_rows = x ? k.inv_rows[1] : k.inv_rows[0];
+    const float cnt0 = (float)fewer, cnt1 = (float)(fewer + 1);
+    const bool whole = rows <= k.res_rows;
 
-    // the widest slab's sizes place the regions, so that they agree within a cluster and a launch
-    const Shape full(a.gps * a.cg, VEC);
-    const size_t keep_bytes = ((size_t)a.res_rows * full.nv * sizeof(Raw) + 15) / 16 * 16;
+    // kept rows | (mean, M2) of each row offset and channel | of each CTA and group | (mean, 1/std) of each group
+    // | the slab's parameters
     Raw* keep = reinterpret_cast<Raw*>(smem);
-    float2* table = reinterpret_cast<float2*>(smem + keep_bytes);
-    float2* part = table + (size_t)VEC * max(full.table(), sh.table());
-    float2* stat = part + a.gps;
+    float2* table = reinterpret_cast<float2*>(smem + k.keep_bytes);
+    float2* part = table + VEC * entries;
+    float2* stat = part + CS * k.gps;
+    float* prm = reinterpret_cast<float*>(smem + k.prm_at);
 
-    const int tid = threadIdx.x, tr = tid / TV, tv = tid - tr * TV;
+    const int tid = threadIdx.x, tr = (int)(((uint32_t)tid * k.inv_tv) >> 20), tv = tid - tr * k.TV;
     const bool active = tr < RP;
+    const int mine = tr < more ? fewer + 1 : fewer;          // this thread's rows per vector
+    const int kept = VEC > 1 ? (whole ? mine : k.res_per) : 0;   // of them kept by an asynchronous copy
     grid_dependents_launch();
     grid_dependency_wait();
 
     // ---- load, keep, accumulate
-    for (int vb = 0; vb < nv; vb += TV) {
+    // the slab's parameters, as [add, gamma, beta][channel]; later [mean - add, gamma / std, beta]
+    // (a slab too wide for that reads them where they are)
+    for (int c = tid; c < k.nprm; c += kThreads) {
+        if (a.add) copy_async4(prm + c, a.add + (size_t)n * C + ch0 + c);
+        else prm[c] = 0.0f;
+        if (a.gamma) copy_async4(prm + k.nch + c, a.gamma + ch0 + c);
+        else prm[k.nch + c] = 1.0f;
+        if (a.beta) copy_async4(prm + 2 * k.nch + c, a.beta + ch0 + c);
+        else prm[2 * k.nch + c] = 0.0f;
+    }
+    for (int vb = 0; vb < nv; vb += k.TV) {
         const int v = vb + tv;
         if (!active || v >= nv) continue;
-        const int ch = ch0 + v * VEC;
-        const bool second = ch >= a.C0;
-        const long ld = second ? a.ld1 : a.ld0;
-        const TI* src = (second ? static_cast<const TI*>(a.x2) + (ch - a.C0) : static_cast<const TI*>(a.x) + ch) +
-                        ((long)n * a.HW + row0) * ld;
-        const size_t limit = (size_t)((long)a.N * a.HW - 1) * ld + (second ? a.C1 : a.C0);   // elements of the source
-        const size_t base = (size_t)((long)n * a.HW + row0) * ld + (second ? ch - a.C0 : ch);
-        float p[VEC], s[VEC], q[VEC];
+        const Source<TI> src(a, row0 + tr, ch0 + v * VEC);
+        const long step = (long)RP * src.ld;
+        Sums<VEC> sums;
+        float e[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) p[i] = s[i] = q[i] = 0.0f;
-        constexpr int U = 4;   // rows in flight per thread
-        bool first = true;
-        int r = tr;
-        for (; r + (U - 1) * RP < rows; r += U * RP) {
-            Raw raw[U];
+        for (int i = 0; i < VEC; ++i) e[i] = 0.0f;
+        sums.start(e);
+        const TI* from = src.p;
+        if constexpr (VEC > 1) {
+            // every kept row's copy is under way before the first is read; a thread reads only what it copied
+            constexpr int kParts = 4;
+            const int per = (kept + kParts - 1) / kParts;
+            Raw* to = keep + tr * nv + v;
+            int i = 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                raw[u] = Raw{};
-                if (in_bounds(base + (size_t)(r + u * RP) * ld + VEC - 1, limit, &g_err))
-                    raw[u] = *reinterpret_cast<const Raw*>(src + (long)(r + u * RP) * ld);
-            }
-            if (first) {
-                V::load(raw[0], p);
-                first = false;
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float x[VEC];
-                V::load(raw[u], x);
-                if (r + u * RP < res) keep[(size_t)(r + u * RP) * nv + v] = raw[u];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float d = x[i] - p[i];
-                    s[i] += d;
-                    q[i] = fmaf(d, d, q[i]);
+            for (int q = 0; q < kParts; ++q) {
+                for (const int end = min(kept, (q + 1) * per); i < end; ++i) {
+                    if (in_bounds(src.base + (size_t)i * step + VEC - 1, src.limit, &g_err)) copy_async(to, from);
+                    from += step;
+                    to += RP * nv;
                 }
+                copy_commit();
             }
         }
-        for (; r < rows; r += RP) {
+        if constexpr (VEC > 1) {
+            constexpr int kParts = 4;
+            const int per = (kept + kParts - 1) / kParts;
+            const Raw* own = keep + tr * nv + v;
+            int i = 0;
+            auto take = [&](int q) {
+                const int end = min(kept, (q + 1) * per);
+                if (q == 0 && kept > 0) {
+                    V::load(*own, e);
+                    sums.start(e);
+                }
+#pragma unroll 4
+                for (; i < end; ++i) {
+                    V::load(*own, e);
+                    sums.add(e);
+                    own += RP * nv;
+                }
+            };
+            copy_wait<3>();
+            take(0);
+            copy_wait<2>();
+            take(1);
+            copy_wait<1>();
+            take(2);
+            copy_wait<0>();
+            take(3);
+        }
+        // rows that are not kept (or, one value at a time, every row)
+        auto fetch = [&](int i) {
             Raw raw = Raw{};
-            if (in_bounds(base + (size_t)r * ld + VEC - 1, limit, &g_err))
-                raw = *reinterpret_cast<const Raw*>(src + (long)r * ld);
-            float x[VEC];
-            V::load(raw, x);
-            if (first) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) p[i] = x[i];
-                first = false;
-            }
-            if (r < res) keep[(size_t)r * nv + v] = raw;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const float d = x[i] - p[i];
-                s[i] += d;
-                q[i] = fmaf(d, d, q[i]);
-            }
+            if (in_bounds(src.base + (size_t)i * step + VEC - 1, src.limit, &g_err))
+                raw = *reinterpret_cast<const Raw*>(src.p + (long)i * step);
+            return raw;
+        };
+        if (kept == 0 && mine > 0) {
+            V::load(fetch(0), e);
+            sums.start(e);
         }
-        const int cnt = tr < rows ? (rows - tr + RP - 1) / RP : 0;
-        const float inv = cnt ? 1.0f / (float)cnt : 0.0f;
+#pragma unroll 4
+        for (int i = kept; i < mine; ++i) {
+            const Raw raw = fetch(i);
+            if (VEC == 1 && (whole || i < k.res_per)) keep[(tr + i * RP) * nv + v] = raw;
+            V::load(raw, e);
+            sums.add(e);
+        }
+        const float inv = tr < more ? inv1 : inv0;
+        float p[VEC], sum[VEC], q[VEC];
+        sums.get(p, sum, q);
+        float2* t = table + tr * k.nvp + v;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const float add = a.add ? a.add[(size_t)n * C + ch + i] : 0.0f;
-            const float dm = s[i] * inv;
-            table[(size_t)i * sh.table() + (size_t)tr * sh.nvp + v] =
-                make_float2(p[i] + dm + add, fmaf(-s[i], dm, q[i]));
+            const float dm = sum[i] * inv;
+            t[i * entries] = make_float2(p[i] + dm, fmaf(-sum[i], dm, q[i]));
+        }
+    }
+    copy_wait<0>();   // (a thread without rows has copied parameters)
+    __syncthreads();
+
+    // ---- join the row offsets of each channel: `lanes` lanes of a warp per channel
+    const int warp = tid >> 5, lane = tid & 31;
+    {
+        const int P = 1 << k.log_lanes, used = min(RP, rows);   // row offsets with at least one row
+        for (int base = 0; base < k.nch; base += kThreads >> k.log_lanes) {
+            const int c = base + (tid >> k.log_lanes), sub = tid & (P - 1);
+            float2* col = table + (int)((unsigned)c % VEC) * entries + (int)((unsigned)c / VEC);
+            float S = 0.0f, Q = 0.0f, pivot = 0.0f;
+            if (c < k.nch) {
+                pivot = col->x;
+#pragma unroll 4
+                for (int ro = sub; ro < used; ro += P) {
+                    const float2 m = col[ro * k.nvp];
+                    const float cnt = ro < more ? cnt1 : cnt0, d = m.x - pivot;
+                    S = fmaf(cnt, d, S);
+                    Q += fmaf(cnt * d, d, m.y);
+                }
+            }
+            for (int o = P >> 1; o > 0; o >>= 1) {
+                S += __shfl_xor_sync(0xffffffffu, S, o);
+                Q += __shfl_xor_sync(0xffffffffu, Q, o);
+            }
+            if (c < k.nch && sub == 0) {   // into the channel's first entry, which its lanes have read
+                const float dm = S * inv_rows;
+                const float add = k.nprm ? prm[c] : (a.add ? a.add[(size_t)n * C + ch0 + c] : 0.0f);
+                *col = make_float2(pivot + dm + add, fmaf(-S, dm, Q));   // (the addend moves the mean alone)
+            }
         }
     }
     __syncthreads();
 
-    // ---- one warp per group: join the (mean, M2) pairs of its channels and row offsets
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int g = warp; g < ng; g += kThreads / 32) {
-        auto entry = [&](int ch, int ro) {   // channel within the slab
-            return table[(size_t)(ch % VEC) * sh.table() + (size_t)ro * sh.nvp + ch / VEC];
+    // every CTA of the cluster has started: its shared memory may be written
+    if (CS > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+
+    // ---- join the channels of each group, each with `rows` values: one warp per group, the mean first
+    for (int g = warp; g < k.gps; g += kThreads / 32) {
+        auto channel = [&](int c) {
+            c += g * k.cg;
+            return table[(int)((unsigned)c % VEC) * entries + (int)((unsigned)c / VEC)];
         };
-        const float pivot = entry(g * a.cg, 0).x;
-        const int used = min(RP, rows);   // row offsets with at least one row
-        float S = 0.0f, Q = 0.0f;
-        for (int e = lane; e < a.cg * used; e += 32) {
-            const int c = e / used, ro = e - c * used;
-            const float2 m = entry(g * a.cg + c, ro);
-            const float cnt = (float)((rows - ro + RP - 1) / RP), d = m.x - pivot;
-            S = fmaf(cnt, d, S);
-            Q += fmaf(cnt * d, d, m.y);
+        const float2 own = lane < k.cg ? channel(lane) : make_float2(0.0f, 0.0f);
+        const float pivot = __shfl_sync(0xffffffffu, own.x, 0);
+        float S = lane < k.cg ? own.x - pivot : 0.0f;
+        for (int c = lane + 32; c < k.cg; c += 32) S += channel(c).x - pivot;
+        const float m = pivot + warp_sum(S) * k.inv_cg_f;
+        float d = own.x - m, Q = lane < k.cg ? fmaf((float)rows * d, d, own.y) : 0.0f;
+        for (int c = lane + 32; c < k.cg; c += 32) {
+            const float2 o = channel(c);
+            d = o.x - m;
+            Q += fmaf((float)rows * d, d, o.y);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            S += __shfl_xor_sync(0xffffffffu, S, o);
-            Q += __shfl_xor_sync(0xffffffffu, Q, o);
-        }
-        if (lane == 0) {
-            const float cnt = (float)rows * (float)a.cg, dm = rows ? S / cnt : 0.0f;
-            part[g] = make_float2(rows ? pivot + dm : 0.0f, fmaf(-S, dm, Q));
-        }
+        Q = warp_sum(Q);
+        // to every CTA of the cluster
+        if (lane < CS) st_cluster(&part[rank * k.gps + g], lane, rows ? make_float2(m, Q) : make_float2(0.0f, 0.0f));
     }
-    if (CS > 1) cg::this_cluster().sync();
+    if (CS > 1) sm100::cluster_sync();
     else __syncthreads();
 
-    // ---- join the CTAs' pairs in rank order
-    for (int g = tid; g < ng; g += kThreads) {
-        const float pivot = (CS > 1 ? ld_cluster(&part[g], 0) : part[g]).x;
-        float S = 0.0f, Q = 0.0f;
-        for (int k = 0; k < CS; ++k) {
-            const float2 m = CS > 1 ? ld_cluster(&part[g], k) : part[g];
-            const float cnt = (float)(a.HW * (k + 1) / CS - a.HW * k / CS) * (float)a.cg, d = m.x - pivot;
-            S = fmaf(cnt, d, S);
-            Q += fmaf(cnt * d, d, m.y);
-        }
-        const float cnt = (float)a.HW * (float)a.cg, dm = S / cnt;
-        float var = fmaf(-S, dm, Q) / cnt;
-        var = var < 0.0f ? 0.0f : var;   // rounding only; a NaN stays
-        stat[g] = make_float2(pivot + dm, 1.0f / sqrtf(var + a.eps));
+    // ---- join the CTAs' pairs: one lane per (group, CTA)
+    for (int base = 0; base < k.gps; base += kThreads >> k.log_cluster) {
+        const int g = base + (tid >> k.log_cluster), r = tid & (CS - 1);
+        const bool on = g < k.gps;
+        float2 m = make_float2(0.0f, 0.0f);
+        if (on) m = part[r * k.gps + g];
+        const float pivot = __shfl_sync(0xffffffffu, m.x, lane & ~(CS - 1));   // the first CTA's mean
+        const float cnt = (float)(k.share + (r < k.extra ? 1 : 0)) * (float)k.cg;
+        float S = cnt * (m.x - pivot);
+        for (int o = CS >> 1; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
+        const float mean = fmaf(S, k.inv_all, pivot), d = m.x - mean;
+        float Q = fmaf(cnt * d, d, m.y);
+        for (int o = CS >> 1; o > 0; o >>= 1) Q += __shfl_xor_sync(0xffffffffu, Q, o);
+        if (on && r == 0) stat[g] = make_float2(mean, 1.0f / sqrtf(fmaf(Q, k.inv_all, a.eps)));
     }
     __syncthreads();
-    // this CTA has read the others' pairs; it leaves only when they have read its own (waited for at the end)
-    if (CS > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    for (int c = tid; c < k.nprm; c += kThreads) {
+        const float2 st = stat[k.inv_cg ? (int)__umulhi((uint32_t)c, k.inv_cg) : c];
+        prm[c] = st.x - prm[c];
+        prm[k.nch + c] *= st.y;
+    }
+    __syncthreads();
 
     // ---- normalise, activate, store
     TO* y = static_cast<TO*>(a.y);
-    for (int vb = 0; vb < nv; vb += TV) {
+    for (int vb = 0; vb < nv; vb += k.TV) {
         const int v = vb + tv;
         if (!active || v >= nv) continue;
         const int ch = ch0 + v * VEC;
-        const bool second = ch >= a.C0;
-        const long ld = second ? a.ld1 : a.ld0;
-        const TI* src = (second ? static_cast<const TI*>(a.x2) + (ch - a.C0) : static_cast<const TI*>(a.x) + ch) +
-                        ((long)n * a.HW + row0) * ld;
-        float m[VEC], A[VEC], B[VEC];
+        float m[VEC], gamma[VEC], beta[VEC];
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const float2 st = stat[(v * VEC + i) / a.cg];
-            m[i] = a.add ? st.x - a.add[(size_t)n * C + ch + i] : st.x;
-            A[i] = st.y * (a.gamma ? a.gamma[ch + i] : 1.0f);
-            B[i] = a.beta ? a.beta[ch + i] : 0.0f;
+            const int c = v * VEC + i;
+            if (k.nprm) {
+                m[i] = prm[c];
+                gamma[i] = prm[k.nch + c];
+                beta[i] = prm[2 * k.nch + c];
+            } else {
+                const float2 st = stat[k.inv_cg ? (int)__umulhi((uint32_t)c, k.inv_cg) : c];
+                m[i] = a.add ? st.x - a.add[(size_t)n * C + ch + i] : st.x;
+                gamma[i] = a.gamma ? a.gamma[ch + i] * st.y : st.y;
+                beta[i] = a.beta ? a.beta[ch + i] : 0.0f;
+            }
         }
-        const size_t ybase = (size_t)((long)n * a.HW + row0) * a.ldy + ch;
+        const size_t ybase = (size_t)(row0 + tr) * a.ldy + ch, ystep = (size_t)RP * a.ldy;
         const size_t ylimit = (size_t)((long)a.N * a.HW - 1) * a.ldy + C;
-#pragma unroll 2
-        for (int r = tr; r < rows; r += RP) {
-            const Raw raw = r < res ? keep[(size_t)r * nv + v] : *reinterpret_cast<const Raw*>(src + (long)r * ld);
-            float x[VEC], o[VEC];
-            V::load(raw, x);
+        auto finish = [&](const Raw& raw, int i) {
+            float o[VEC];
+            V::load(raw, o);
+            if constexpr (VEC > 1) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) o[i] = activate<FAST>(fmaf(x[i] - m[i], A[i], B[i]), a.act);
-            const size_t yi = ybase + (size_t)r * a.ldy;
-            if (in_bounds(yi + VEC - 1, ylimit, &g_err)) store<TO, VEC>(y + yi, o, a.vec_y != 0);
+                for (int j = 0; j < VEC; j += 2)
+                    f2_unpack(f2_fma(f2_sub(f2_pack(o[j], o[j + 1]), f2_pack(m[j], m[j + 1])), f2_pack(gamma[j], gamma[j + 1]),
+                                     f2_pack(beta[j], beta[j + 1])),
+                              o[j], o[j + 1]);
+            } else {
+                o[0] = fmaf(o[0] - m[0], gamma[0], beta[0]);
+            }
+            activate_all<ACT, FAST>(o);
+            const size_t yi = ybase + (size_t)i * ystep;
+            if (in_bounds(yi + VEC - 1, ylimit, &g_err)) store<TO, VEC>(y + yi, o, k.vec_y);
+        };
+        const int held = whole ? mine : k.res_per;
+        const Raw* own = keep + tr * nv + v;
+        int i = 0;
+#pragma unroll 1   // (a row's eight values are independent work enough; two rows would not fit in registers)
+        for (; i < held; ++i) finish(own[i * RP * nv], i);
+        if (held < mine) {
+            const Source<TI> src(a, row0 + tr, ch);
+            const long step = (long)RP * src.ld;
+#pragma unroll 4
+            for (i = held; i < mine; ++i) finish(*reinterpret_cast<const Raw*>(src.p + (long)i * step), i);
         }
     }
-    if (CS > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 
-// Shared memory of a CTA beside its kept rows.
-size_t table_bytes(int groups, int cg, int gps, int vec) {
-    // a narrower last slab has more row offsets, so its table can be larger
-    const int last = groups - (groups - 1) / gps * gps;
-    const size_t table = std::max(Shape(gps * cg, vec).table(), Shape(last * cg, vec).table());
-    return sizeof(float2) * (vec * table + 2 * (size_t)gps);
+// Fills in what does not depend on pointers; the shared memory that the split needs.
+size_t make_split(const GroupNormArgs& a, int vec, const GroupNormSplit& s, Split* out) {
+    Split k = {};
+    const int C = a.C0 + a.C1, es = a.x_bf16 ? 2 : 4;
+    k.cg = C / a.groups;
+    k.gps = s.gps;
+    k.cluster = s.cluster;
+    k.slabs = a.groups / s.gps;
+    k.nch = k.gps * k.cg;
+    k.nv = k.nch / vec;
+    k.TV = std::min(k.nv, kThreads);
+    k.RP = kThreads / k.TV;
+    k.nvp = k.nv | 1;
+    k.entries = k.RP * k.nvp;
+    k.inv_tv = ((1u << 20) + k.TV - 1) / k.TV;
+    k.inv_cg = k.cg == 1 ? 0u : (uint32_t)(((1ull << 32) + k.cg - 1) / k.cg);
+    while ((1 << k.log_cluster) < s.cluster) ++k.log_cluster;
+    while (k.log_lanes < 5 && (2 << k.log_lanes) * (long)k.nch <= kThreads && (2 << k.log_lanes) <= k.RP) ++k.log_lanes;
+    k.share = (int)(a.HW / s.cluster);
+    k.extra = (int)(a.HW - (long)k.share * s.cluster);
+    const int most = k.share + (k.extra ? 1 : 0);
+    for (int x = 0; x < 2; ++x) {
+        const int rows = k.share + x;
+        k.fewer[x] = rows / k.RP;
+        k.more[x] = rows - k.fewer[x] * k.RP;
+        k.inv0[x] = k.fewer[x] ? 1.0f / (float)k.fewer[x] : 0.0f;
+        k.inv1[x] = 1.0f / (float)(k.fewer[x] + 1);
+        k.inv_rows[x] = rows ? 1.0f / (float)rows : 0.0f;
+    }
+    k.inv_cg_f = 1.0f / (float)k.cg;
+    k.inv_all = (float)(1.0 / ((double)a.HW * k.cg));
+    const long row_bytes = (long)k.nch * es;
+    if (most * row_bytes <= kResBytes) {
+        k.res_rows = most;
+    } else {
+        k.res_per = (int)(kResBytes / row_bytes / k.RP);
+        k.res_rows = k.res_per * k.RP;
+    }
+    k.keep_bytes = (int)((k.res_rows * row_bytes + 15) / 16 * 16);
+    const size_t prm_at =
+        ((size_t)k.keep_bytes + sizeof(float2) * ((size_t)vec * k.entries + (size_t)(s.cluster + 1) * k.gps) + 15) / 16 * 16;
+    k.prm_at = (int)prm_at;
+    k.nprm = k.nch <= kMaxParams ? k.nch : 0;
+    if (out) *out = k;
+    return prm_at + 3 * sizeof(float) * (size_t)k.nprm;
 }
 
-size_t smem_bytes(const GroupNormArgs& a, int vec, int es) {
-    return ((size_t)a.res_rows * a.gps * a.cg * es + 15) / 16 * 16 + table_bytes(a.groups, a.cg, a.gps, vec);
-}
-
-template <typename TI, typename TO, int VEC>
-cudaError_t launch(const GroupNormArgs& a, int cluster, cudaStream_t st) {
+template <typename TI, typename TO, int VEC, int ACT>
+cudaError_t launch(const GroupNormArgs& a, const Split& k, size_t smem, cudaStream_t st) {
     static bool done[64], done_cluster[64];
-    auto kern = group_norm_kernel<TI, TO, VEC>;
-    const size_t smem = smem_bytes(a, VEC, (int)sizeof(TI));
+    auto kern = group_norm_kernel<TI, TO, VEC, ACT>;
     cudaError_t e = allow_smem(kern, 227 * 1024, done);
     if (e != cudaSuccess) return e;
-    if (cluster > 8) {
+    if (k.cluster > 8) {
         int dev = 0;
         if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
         if (dev < 0 || dev >= 64 || !done_cluster[dev]) {
@@ -339,8 +540,9 @@ cudaError_t launch(const GroupNormArgs& a, int cluster, cudaStream_t st) {
             if (dev >= 0 && dev < 64) done_cluster[dev] = true;
         }
     }
+    constexpr int kMaxY = 65535;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((long)a.N * a.slabs * cluster));
+    cfg.gridDim = dim3((unsigned)(k.slabs * k.cluster), (unsigned)std::min(a.N, kMaxY), (unsigned)((a.N + (long)kMaxY - 1) / kMaxY));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -348,17 +550,25 @@ cudaError_t launch(const GroupNormArgs& a, int cluster, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.x = (unsigned)k.cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, a);
+    cfg.numAttrs = k.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, a, k);
+}
+
+template <typename TI, typename TO, int VEC>
+cudaError_t launch_act(const GroupNormArgs& a, const Split& k, size_t smem, cudaStream_t st) {
+    switch (a.act) {
+        case WINO_ACT_SILU: return launch<TI, TO, VEC, WINO_ACT_SILU>(a, k, smem, st);
+        case WINO_ACT_GELU: return launch<TI, TO, VEC, WINO_ACT_GELU>(a, k, smem, st);
+        default: return launch<TI, TO, VEC, WINO_ACT_NONE>(a, k, smem, st);
+    }
 }
 
 template <typename TI, typename TO>
-cudaError_t launch_vec(const GroupNormArgs& a, bool vec, int cluster, cudaStream_t st) {
-    constexpr int VEC = 16 / (int)sizeof(TI);
-    return vec ? launch<TI, TO, VEC>(a, cluster, st) : launch<TI, TO, 1>(a, cluster, st);
+cudaError_t launch_vec(const GroupNormArgs& a, bool vec, const Split& k, size_t smem, cudaStream_t st) {
+    return vec ? launch_act<TI, TO, 16 / (int)sizeof(TI)>(a, k, smem, st) : launch_act<TI, TO, 1>(a, k, smem, st);
 }
 
 bool aligned(const void* p, long ld_bytes, size_t to) {
@@ -367,52 +577,52 @@ bool aligned(const void* p, long ld_bytes, size_t to) {
 
 }  // namespace
 
-// The widest slab (long contiguous runs) and the smallest cluster whose CTAs' shares fit in shared
-// memory and that make two CTAs per SM; when no split does both, the one with the smallest share.
+// The split with the least estimated time: rounds of two CTAs per SM, each a fixed part (launch, joins, exchange)
+// plus its share of the input.  The constants are fits to measured splits (in us; 8 x 64 x 64 x 320 bf16 with SiLU takes
+// 16.1 as 256 CTAs of 82 KiB in clusters of 8, 21.3 as 512 of 41 KiB; 8 x 32 x 32 x 640 9.9 in clusters of 4, 22.3
+// in clusters of 16, which leave SMs idle).
 GroupNormSplit group_norm_split(const GroupNormArgs& a, int vec, int num_sms) {
     const int cg = (a.C0 + a.C1) / a.groups, es = a.x_bf16 ? 2 : 4;
-    const int unit = std::min(a.groups, vec / gcd(cg, vec));   // groups of the narrowest slab of whole vectors
-    const int units = (a.groups + unit - 1) / unit;
+    const int unit = vec / gcd(cg, vec);   // groups of the narrowest slab of whole vectors
     GroupNormSplit best = {a.groups, 1};
-    double best_bytes = 0;
-    for (int s = 1; s <= units; ++s) {
-        const int per = (units + s - 1) / s;
-        if (s > 1 && per == (units + s - 2) / (s - 1)) continue;   // the same slabs
-        const int gps = std::min(a.groups, per * unit);
-        if (gps > unit && table_bytes(a.groups, cg, gps, vec) > 64 * 1024) continue;
+    double best_cost = 1e30;
+    for (int slabs = 1; slabs <= a.groups; ++slabs) {
+        if (a.groups % slabs != 0) continue;
+        const int gps = a.groups / slabs;
+        if (gps != a.groups && gps % unit != 0) continue;
         for (int c = 1; c <= kMaxCluster; c *= 2) {
             if (c > 1 && c > a.HW) break;
-            const double bytes = (double)((a.HW + c - 1) / c) * gps * cg * es;
-            const long ctas = (long)a.N * ((a.groups + gps - 1) / gps) * c;
-            if (bytes <= kResBytes && (ctas >= 2 * num_sms || bytes <= 8 * 1024)) return {gps, c};
-            if (best_bytes == 0 || bytes < best_bytes) {
-                best_bytes = bytes;
-                best = {gps, c};
-            }
+            const double kb = (double)((a.HW + c - 1) / c) * gps * cg * es / 1024.0;
+            const double ctas = (double)a.N * slabs * c, full = 2.0 * num_sms, fill = std::min(1.0, ctas / full);
+            double cost = 4.0 + 0.1 * kb * (0.6 + 0.4 * fill) + 0.08 * ((gps + 7) / 8);
+            if (kb > kResBytes / 1024) cost += 0.05 * (kb - kResBytes / 1024);
+            if (c > 1) cost += 0.5 + (c > 4 ? 0.24 : 0.16);
+            if (c > 8) cost *= ctas > num_sms ? 1.6 : 1.05;
+            if (gps * cg * es < 64) cost *= 1.3;   // rows of less than two sectors
+            cost *= std::max(1.0, ctas / full);
+            if (cost >= best_cost) continue;
+            if (gps * cg > kMaxParams && make_split(a, vec, {gps, c}, nullptr) > 227 * 1024) continue;
+            best_cost = cost;
+            best = {gps, c};
         }
     }
     return best;
 }
 
-cudaError_t launch_group_norm(GroupNormArgs a, int num_sms, const GroupNormSplit* split, cudaStream_t st) {
+cudaError_t launch_group_norm(const GroupNormArgs& a, int num_sms, const GroupNormSplit* split, cudaStream_t st) {
     const int C = a.C0 + a.C1, es = a.x_bf16 ? 2 : 4, eo = a.y_bf16 ? 2 : 4, VEC = 16 / es;
-    a.cg = C / a.groups;
     const bool vec = C % VEC == 0 && a.C0 % VEC == 0 && aligned(a.x, a.ld0 * es, 16) &&
                      (a.C1 == 0 || aligned(a.x2, a.ld1 * es, 16));
-    const size_t out_vec = (size_t)std::min(16, VEC * eo);
-    a.vec_y = aligned(a.y, a.ldy * eo, out_vec) ? 1 : 0;
     const GroupNormSplit s = split ? *split : group_norm_split(a, vec ? VEC : 1, num_sms);
-    a.gps = s.gps;
-    a.slabs = (a.groups + s.gps - 1) / s.gps;
-    const long share = (a.HW + s.cluster - 1) / s.cluster;
-    a.res_rows = (int)std::min<long>(share, kResBytes / ((long)a.gps * a.cg * es));
-    if (smem_bytes(a, vec ? VEC : 1, es) > 227 * 1024 || (double)a.N * a.slabs * s.cluster > 2147483647.0)
-        return cudaErrorInvalidConfiguration;
+    Split k;
+    const size_t smem = make_split(a, vec ? VEC : 1, s, &k);
+    if (smem > 227 * 1024 || a.N > 1000000000) return cudaErrorInvalidConfiguration;
+    k.vec_y = aligned(a.y, a.ldy * eo, (size_t)std::min(16, VEC * eo));
     if (a.x_bf16)
-        return a.y_bf16 ? launch_vec<__nv_bfloat16, __nv_bfloat16>(a, vec, s.cluster, st)
-                        : launch_vec<__nv_bfloat16, float>(a, vec, s.cluster, st);
-    return a.y_bf16 ? launch_vec<float, __nv_bfloat16>(a, vec, s.cluster, st)
-                    : launch_vec<float, float>(a, vec, s.cluster, st);
+        return a.y_bf16 ? launch_vec<__nv_bfloat16, __nv_bfloat16>(a, vec, k, smem, st)
+                        : launch_vec<__nv_bfloat16, float>(a, vec, k, smem, st);
+    return a.y_bf16 ? launch_vec<float, __nv_bfloat16>(a, vec, k, smem, st)
+                    : launch_vec<float, float>(a, vec, k, smem, st);
 }
 
 cudaError_t group_norm_take_error(int* err) {

@@ -65,7 +65,9 @@ __global__ void __launch_bounds__(kThreads) matmul_simt_kernel(const MatmulArgs 
         for (int j = 0; j < 4; ++j) {
             const int m = m0 + tm + i, n = n0 + tn + j;
             if (m >= p.M || n >= p.N) continue;
-            float v = activate<sizeof(TO) == 2>(acc[i][j] + (p.bias ? p.bias[n] : 0.0f), p.act);
+            float v = acc[i][j] + (p.bias ? p.bias[n] : 0.0f);
+            if (p.act == WINO_ACT_SILU) v = activate<WINO_ACT_SILU, sizeof(TO) == 2>(v);
+            if (p.act == WINO_ACT_GELU) v = activate<WINO_ACT_GELU, sizeof(TO) == 2>(v);
             const size_t at = (size_t)m * p.ldo + n;
             if (!in_bounds(at, (size_t)(p.M - 1) * p.ldo + p.N, &g_err)) continue;
             if (p.res) v += to_f32(static_cast<const TO*>(p.res)[(size_t)m * p.ldr + n]);

@@ -297,13 +297,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     v[j + 2] = __uint_as_float(r[j + 2]) + bb.z;
                     v[j + 3] = __uint_as_float(r[j + 3]) + bb.w;
                 }
-                if (p.m.act == WINO_ACT_SILU) {
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) v[j] = silu<sizeof(TO) == 2>(v[j]);
-                } else if (p.m.act == WINO_ACT_GELU) {
-#pragma unroll
-                    for (int j = 0; j < kChunk; ++j) v[j] = activate<sizeof(TO) == 2>(v[j], WINO_ACT_GELU);
-                }
+                if (p.m.act == WINO_ACT_SILU) activate_all<WINO_ACT_SILU, sizeof(TO) == 2>(v);
+                if (p.m.act == WINO_ACT_GELU) activate_all<WINO_ACT_GELU, sizeof(TO) == 2>(v);
                 if (!DIRECT && !warp_wait(&tail->buf_full[g][buf], rphase, abort_flag)) {
                     ok = false;
                     break;

@@ -9,25 +9,84 @@
 #include <cstdint>
 
 #include "../../include/wino.h"
+#include "common.cuh"
 
 namespace wino {
 
 // ------------------------------------------------------------ activations
-// SiLU and GELU (erf form) in fp32.  FAST: the result is rounded to bf16 next, so the approximate
+// SiLU v / (1 + exp(-v)) and GELU v Phi(v) in fp32.  FAST: the result is rounded to bf16 next, so the hardware's
 // exponential and reciprocal (relative error below 2^-20, bf16 rounds at 2^-9) serve; otherwise the
 // accurate expf and an IEEE division.
-template <bool FAST>
-__device__ __forceinline__ float silu(float v) {
-    // exp(-v) = inf (v below about -88) gives v * (1 / inf) = -0
-    if (FAST) return __fdividef(1.0f, 1.0f + __expf(-v)) * v;
-    return v / (1.0f + expf(-v));
+__device__ __forceinline__ float exp2_fast(float v) {   // results below 2^-126 become 0
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float reciprocal(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 template <bool FAST>
-__device__ __forceinline__ float activate(float v, int act) {
-    if (act == WINO_ACT_SILU) return silu<FAST>(v);
-    if (act == WINO_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);
+__device__ __forceinline__ float silu(float v) {
+    // exp(-v) = inf (v below about -88) gives v * (1 / inf) = -0
+    if (FAST) return reciprocal(1.0f + exp2_fast(v * -1.4426950408889634f)) * v;
+    return v / (1.0f + expf(-v));
+}
+
+template <int ACT, bool FAST>
+__device__ __forceinline__ float activate(float v) {
+    if (ACT == WINO_ACT_SILU) return silu<FAST>(v);
+    if (ACT == WINO_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);
     return v;
+}
+
+// min of three, NaN if one is NaN.
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Activates N values.  FAST SiLU takes one reciprocal for four values, since the special-function unit is its
+// bound (1.25 operations there per value instead of 2), and its products in packed pairs: with E = 1 + exp(-v),
+// X = (E0 E2, E1 E3) and r = 1 / (X0 X1), the reciprocals of (E0, E1) are (r X1, r X0) (E2, E3) and those of (E2, E3)
+// the same pair times (E0, E1).  With every value above -21 the product of four stays below 2^124; otherwise
+// (or with a NaN, which must not reach its neighbours) each value goes alone.
+template <int ACT, bool FAST, int N>
+__device__ __forceinline__ void activate_all(float (&v)[N]) {
+    if constexpr (ACT == WINO_ACT_SILU && FAST && N % 4 == 0) {
+        // (the check comes after the fast results, so that they do not wait for it)
+        const uint64_t scale = f2_pack(-1.4426950408889634f, -1.4426950408889634f), one = f2_pack(1.0f, 1.0f);
+        float w[N], lo[N / 4];
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint64_t va = f2_pack(v[i], v[i + 1]), vb = f2_pack(v[i + 2], v[i + 3]);
+            float t0, t1, t2, t3, x0, x1;
+            f2_unpack(f2_mul(va, scale), t0, t1);
+            f2_unpack(f2_mul(vb, scale), t2, t3);
+            const uint64_t ea = f2_add(f2_pack(exp2_fast(t0), exp2_fast(t1)), one);
+            const uint64_t eb = f2_add(f2_pack(exp2_fast(t2), exp2_fast(t3)), one);
+            f2_unpack(f2_mul(ea, eb), x0, x1);
+            const float r = reciprocal(x0 * x1);
+            const uint64_t y = f2_pack(r * x1, r * x0);
+            f2_unpack(f2_mul(va, f2_mul(y, eb)), w[i], w[i + 1]);
+            f2_unpack(f2_mul(vb, f2_mul(y, ea)), w[i + 2], w[i + 3]);
+            lo[i / 4] = min3_nan(min3_nan(v[i], v[i + 1], v[i + 2]), v[i + 3], v[i + 3]);
+        }
+#pragma unroll
+        for (int i = 1; i < N / 4; i += 2) lo[0] = min3_nan(lo[0], lo[i], i + 1 < N / 4 ? lo[i + 1] : lo[i]);
+        if (!(lo[0] > -21.0f)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i] = silu<true>(v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = w[i];
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = activate<ACT, FAST>(v[i]);
 }
 
 // ------------------------------------------------------------ group norm
@@ -43,12 +102,6 @@ struct GroupNormArgs {
     int N, C0, C1, groups, act;
     float eps;
     bool x_bf16, y_bf16;
-    // set by the launcher
-    int cg;                // channels per group
-    int gps;               // groups per slab
-    int slabs;             // slabs per image
-    int vec_y;             // 1: rows of y take whole-vector stores
-    int res_rows;          // rows of a CTA kept in shared memory
 };
 
 // How a call is cut: a cluster of `cluster` CTAs per (image, slab of `gps` groups).
@@ -57,7 +110,7 @@ struct GroupNormSplit {
 };
 GroupNormSplit group_norm_split(const GroupNormArgs& a, int vec, int num_sms);
 // split: null for the rule's choice.
-cudaError_t launch_group_norm(GroupNormArgs a, int num_sms, const GroupNormSplit* split, cudaStream_t st);
+cudaError_t launch_group_norm(const GroupNormArgs& a, int num_sms, const GroupNormSplit* split, cudaStream_t st);
 
 // --------------------------------------------------------- matrix product
 struct MatmulArgs {
