@@ -1,5 +1,6 @@
 """Build the CUDA library in-tree: group_wise_int8_b200/libwino_b200.so (sm_100a),
-and its debug build libwino_b200_debug.so.
+its debug build libwino_b200_debug.so, and torch_ops_b200.so, the compiled marshalling of torch tensors for the
+operators beside the convolution.
 
     python -m group_wise_int8_b200.build [--force] [--verbose]
 
@@ -27,6 +28,7 @@ SOURCES = ["plan.cpp", "api.cu", "weight_transform.cu", "input_transform.cu", "h
            "hadamard_simt.cu", "output_transform.cu", "input_quant.cu", "noalloc.cu", "fused_small.cu",
            "ops_api.cu", "group_norm.cu", "matmul_simt.cu", "matmul_tc.cu"]
 HEADERS = ["plan.h", "common.cuh", "sm100.cuh", "kernels.h", "ops.h"]
+TORCH_OPS = os.path.join(HERE, "torch_ops_b200.so")   # torch marshalling of the operators beside the convolution
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -79,11 +81,32 @@ def _build_one(lib: str, debug: bool, verbose: bool, ex) -> None:
     os.replace(tmp, lib)
 
 
+def _build_torch_ops(src: str) -> None:
+    """The CPython module of csrc/torch_ops.cpp, against the installed torch (whose libraries are loaded before it)."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+    inc = include_paths() + [os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_OPS + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-shared", "-std=c++17", "-O2", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           *["-isystem" + i for i in inc], src, "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for torch_ops.cpp:\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(tmp, TORCH_OPS)
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = True) -> str:
-    """Builds whichever of the release and (with debug) the debug library is out of date; returns
+    """Builds whichever of the release and (with debug) the debug library and the torch module is out of date; returns
     the release path."""
     libs = ((LIB, False), (LIB_DEBUG, True)) if debug else ((LIB, False),)
     todo = [(lib, dbg) for lib, dbg in libs if force or not up_to_date(lib)]
+    torch_ops_src = [os.path.join(CSRC, "torch_ops.cpp"), os.path.join(ROOT, "include", "wino.h"), os.path.abspath(__file__)]
+    if force or not (os.path.exists(TORCH_OPS) and
+                     all(os.path.getmtime(f) <= os.path.getmtime(TORCH_OPS) for f in torch_ops_src)):
+        _build_torch_ops(torch_ops_src[0])
     if todo:
         with concurrent.futures.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 1)) as ex:
             for lib, dbg in todo:

@@ -313,72 +313,42 @@ class Plan:
 # ------------------------------------------------- operators beside the convolution
 _GROUP_NORM_ARGS = struct.Struct("@6P3q2i6iif")   # wino_group_norm_args
 _MATMUL_ARGS = struct.Struct("@6P5q2i4i2i")       # wino_matmul_args
-_DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: F32}
+TORCH_OPS_PATH = os.path.join(HERE, "torch_ops_b200.so")
+
+_ops = {}   # variant -> (module, True for the debug library)
 
 
-def _operand(name: str, t: torch.Tensor, device: torch.device, dtype: Optional[torch.dtype] = None) -> int:
-    """Checks a tensor of a call on `device` and returns its address."""
-    if t.device != device:
-        raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError("%s is %s, not %s" % (name, t.dtype, dtype))
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError("%s requires grad: this operator has no backward pass (call it under torch.no_grad())" % name)
-    return t.data_ptr()
+def load_torch_ops(variant: str = "release"):
+    """The compiled marshalling of group_norm and matmul (csrc/torch_ops.cpp), bound to a build of the library; raises
+    OSError if it has not been built."""
+    if variant not in _ops:
+        L = load_library(variant=variant)
+        if not os.path.exists(TORCH_OPS_PATH):
+            raise OSError("%s is missing: run `python -m group_wise_int8_b200.build`" % TORCH_OPS_PATH)
+        import importlib.util
+        spec = importlib.util.spec_from_file_location("torch_ops_b200", TORCH_OPS_PATH)
+        m = next((m for m, _ in _ops.values()), None)
+        if m is None:
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+        m.set_entries(variant == "debug", ctypes.cast(L.wino_group_norm, _vp).value, ctypes.cast(L.wino_matmul, _vp).value)
+        _ops[variant] = m, variant == "debug"
+    return _ops[variant]
 
 
-def _param(name: str, t: Optional[torch.Tensor], device: torch.device, shape: tuple) -> int:
-    """A contiguous fp32 parameter of the given shape, or None (address 0)."""
-    if t is None:
-        return 0
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous tensor of shape %s" % (name, tuple(shape)))
-    return _operand(name, t, device, torch.float32)
-
-
-def _pitch(name: str, t: torch.Tensor) -> int:
-    """Elements between consecutive rows (the last dimension's vectors) of t: its leading dimensions
-    must collapse into one."""
-    shape, stride = t.shape, t.stride()
-    if stride[-1] != 1 and shape[-1] != 1:
-        raise ValueError("%s: the last dimension must be contiguous" % name)
-    pitch, rows = 0, 1   # of the dimensions seen so far, innermost first
-    for i in range(len(shape) - 2, -1, -1):
-        if shape[i] == 1:
-            continue
-        if rows == 1:
-            pitch = stride[i]
-        elif stride[i] != pitch * rows:
-            raise ValueError("%s: rows must be evenly spaced (got strides %s)" % (name, tuple(stride)))
-        rows *= shape[i]
-    return pitch if rows > 1 else shape[-1]
-
-
-def _run_op(fn, what: str, packed: bytes, device: torch.device, stream, L):
-    """Calls fn with its packed arguments on `stream` (default: the device's current stream)."""
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if device.index == torch.cuda.current_device():
-        rc = fn(packed, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(packed, handle)
-    if rc != OK:
-        raise WinoError(rc, what, L.wino_last_cuda_error(None))
-
-
-def _new_output(shape, dtype, device, stream):
-    """An output for work on `stream`, from that stream's memory pool."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _on_stream(stream, f, tensors):
+    """f() with `stream` current: its output comes from that stream's memory pool, and the tensors' memory is not
+    handed out again before the work on that stream is over."""
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _hold(stream, *tensors):
-    """Tensors used on an explicit stream: their memory is not handed out again before that use is over."""
+        r = f()
     for t in tensors:
         if t is not None:
             t.record_stream(stream)
+    return r
+
+
+def _failed(status: int, what: str, variant: str):
+    return WinoError(status, what, load_library(variant=variant).wino_last_cuda_error(None))
 
 
 def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,
@@ -389,39 +359,19 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
     """act(group_norm([x | x2] + add) * gamma + beta) of NHWC activations (wino_group_norm).
 
     x: [N][H][W][C] bf16/fp32 (a channel range of a wider tensor is fine); x2: [N][H][W][C2] of the same type, the
-    channels after x's without a concatenation; add: fp32 [N][C + C2]; gamma, beta: fp32 [C + C2]; act: ACT_*.
-    out may be x (in place, when there is no x2).  Forward only."""
-    L = _libs.get(LIB_PATHS[variant]) or load_library(variant=variant)
-    if not x.is_cuda or x.dim() != 4:
-        raise ValueError("x must be a CUDA tensor [N][H][W][C]")
-    N, H, W, C = x.shape
-    device, dtype = x.device, x.dtype
-    C2 = p2 = pitch2 = 0
-    if x2 is not None:
-        if x2.dim() != 4 or x2.shape[:3] != x.shape[:3]:
-            raise ValueError("x2 must be [N][H][W][C2] with x's N, H, W")
-        C2, pitch2 = x2.shape[3], _pitch("x2", x2)
-        p2 = _operand("x2", x2, device, dtype)
-    code = _DTYPE_CODES.get(dtype)
-    if code is None:
-        raise ValueError("unsupported dtype %s" % dtype)
-    px = _operand("x", x, device)
-    pa = _param("add", add, device, (N, C + C2))
-    pg, pb = _param("gamma", gamma, device, (C + C2,)), _param("beta", beta, device, (C + C2,))
-    if out is None:
-        out = _new_output((N, H, W, C + C2), out_dtype or dtype, device, stream)
-    elif out.shape != (N, H, W, C + C2) or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError("out must be [N][H][W][C + C2] of out_dtype")
-    ocode = _DTYPE_CODES.get(out.dtype)
-    if ocode is None:
-        raise ValueError("unsupported output dtype %s" % out.dtype)
-    po = _operand("out", out, device)
-    packed = _GROUP_NORM_ARGS.pack(px, p2, pa, pg, pb, po, _pitch("x", x), pitch2, _pitch("out", out), code, ocode,
-                                   N, H, W, C, C2, groups, act, eps)
-    _run_op(L.wino_group_norm, "wino_group_norm", packed, device, stream, L)
-    if stream is not None:
-        _hold(stream, x, x2, add, gamma, beta, out)
-    return out
+    channels after x's without a concatenation; add: fp32 [N][C + C2]; gamma, beta: fp32 [C + C2]; act: ACT_*;
+    out_dtype: bf16 or fp32 (default: out's, else x's).  out may be x (in place, when there is no x2).  Runs on x's
+    device, on its current stream unless one is given.  Forward only: inputs that require grad are refused while
+    gradients are recorded.  Raises ValueError for tensors that do not fit, WinoError for what the library refuses."""
+    m, debug = _ops.get(variant) or load_torch_ops(variant)
+    if stream is None:
+        r = m.group_norm(x, groups, gamma, beta, eps, act, add, x2, out, out_dtype, debug)
+    else:
+        r = _on_stream(stream, lambda: m.group_norm(x, groups, gamma, beta, eps, act, add, x2, out, out_dtype, debug),
+                       (x, x2, add, gamma, beta, out))
+    if r.__class__ is int:
+        raise _failed(r, "wino_group_norm", variant)
+    return r
 
 
 def matmul(a: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: int = ACT_NONE,
@@ -433,47 +383,16 @@ def matmul(a: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None
 
     a: [...][K] bf16/fp32; a2: [...][K2] of the same type, the columns after a's; w: [Nout][K + K2] of the same type;
     bias: fp32 [Nout]; residual: [...][Nout] of the output's type (may be out); act: ACT_*; out_dtype: bf16 or fp32
-    (default: out's or residual's type, else a's).  Forward only."""
-    L = _libs.get(LIB_PATHS[variant]) or load_library(variant=variant)
-    if not a.is_cuda or a.dim() < 1 or w.dim() != 2:
-        raise ValueError("a must be a CUDA tensor [...][K] and w [Nout][K + K2]")
-    lead, K = a.shape[:-1], a.shape[-1]
-    device, dtype = a.device, a.dtype
-    code = _DTYPE_CODES.get(dtype)
-    if code is None:
-        raise ValueError("unsupported dtype %s" % dtype)
-    K2 = p2 = pitch2 = pr = rpitch = 0
-    if a2 is not None:
-        if a2.shape[:-1] != lead:
-            raise ValueError("a2 must have a's leading dimensions")
-        K2, pitch2 = a2.shape[-1], _pitch("a2", a2)
-        p2 = _operand("a2", a2, device, dtype)
-    Nout = w.shape[0]
-    if w.shape[1] != K + K2:
-        raise ValueError("w has %d columns, not %d" % (w.shape[1], K + K2))
-    pa, pw = _operand("a", a, device), _operand("w", w, device, dtype)
-    pb = _param("bias", bias, device, (Nout,))
-    shape = (*lead, Nout)
-    if out is None:
-        if out_dtype is None:
-            out_dtype = dtype if residual is None else residual.dtype
-        out = _new_output(shape, out_dtype, device, stream)
-    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError("out must be [...][Nout] of out_dtype")
-    ocode = _DTYPE_CODES.get(out.dtype)
-    if ocode is None:
-        raise ValueError("unsupported output dtype %s" % out.dtype)
-    if residual is not None:
-        if residual.shape != shape:
-            raise ValueError("residual must be [...][Nout]")
-        pr, rpitch = _operand("residual", residual, device, out.dtype), _pitch("residual", residual)
-    po = _operand("out", out, device)
-    packed = _MATMUL_ARGS.pack(pa, p2, pw, pb, pr, po, _pitch("a", a), pitch2, _pitch("w", w), rpitch,
-                               _pitch("out", out), code, ocode, a.numel() // K if K else 0, Nout, K, K2, act, 0)
-    _run_op(L.wino_matmul, "wino_matmul", packed, device, stream, L)
-    if stream is not None:
-        _hold(stream, a, a2, w, bias, residual, out)
-    return out
+    (default: out's or residual's type, else a's).  Stream, gradients and errors as in group_norm."""
+    m, debug = _ops.get(variant) or load_torch_ops(variant)
+    if stream is None:
+        r = m.matmul(a, w, bias, act, residual, a2, out, out_dtype, debug)
+    else:
+        r = _on_stream(stream, lambda: m.matmul(a, w, bias, act, residual, a2, out, out_dtype, debug),
+                       (a, a2, w, bias, residual, out))
+    if r.__class__ is int:
+        raise _failed(r, "wino_matmul", variant)
+    return r
 
 
 def check_device_error_ops(stream=None, variant: str = "release") -> int:

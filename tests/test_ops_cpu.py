@@ -136,15 +136,16 @@ def test_binding_refuses_host_tensors(lib):
         wino.matmul(torch.zeros(4, 32), torch.zeros(8, 32))
 
 
-def test_row_pitch_of_views():
+def test_row_pitch_of_views(lib):
+    pitch = wino.load_torch_ops()[0].pitch
     t = torch.zeros(2, 3, 4, 40)
-    assert wino._pitch("t", t) == 40
-    assert wino._pitch("t", t[..., 8:24]) == 40
-    assert wino._pitch("t", t[:1, :1, :1]) == 40            # one row: its own length
-    assert wino._pitch("t", t[:, :, ::2]) == 80
+    assert pitch(t) == 40
+    assert pitch(t[..., 8:24]) == 40
+    assert pitch(t[:1, :1, :1]) == 40                       # one row: its own length
+    assert pitch(t[:, :, ::2]) == 80
     with pytest.raises(ValueError, match="evenly"):
-        wino._pitch("t", t[:, :, :3])
+        pitch(t[:, :, :3])
     with pytest.raises(ValueError, match="contiguous"):
-        wino._pitch("t", t.transpose(2, 3))
-    assert wino._pitch("t", torch.zeros(5, 1)[:, :1]) == 1
-    assert wino._pitch("t", torch.zeros(7)) == 7
+        pitch(t.transpose(2, 3))
+    assert pitch(torch.zeros(5, 1)[:, :1]) == 1
+    assert pitch(torch.zeros(7)) == 7
