@@ -81,14 +81,17 @@ struct Tail {
     int abort_flag;
 };
 
+// Warp-uniform bounded wait: every lane polls, the loop exits for all lanes together.  (The timer is read only once a
+// few polls have failed: reading it costs more than most waits.)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
-    const unsigned long long t0 = globaltimer();
+    unsigned long long t0 = 0;
     for (uint32_t it = 0;; ++it) {
-        const bool ok = mbar_try_wait(bar, parity);
-        if (__all_sync(0xffffffffu, ok)) return true;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if ((it & 63u) == 63u) {
             bool stop = *abort_flag != 0;
-            if (!stop && globaltimer() - t0 > kWaitLimitNs) {
+            if (it == 63u) {
+                t0 = globaltimer();
+            } else if (!stop && globaltimer() - t0 > kWaitLimitNs) {
                 stop = true;
                 *abort_flag = 1;
                 atomicCAS(&g_err, 0, kDevErrTimeout);
@@ -167,35 +170,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            int st = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int t = first; ok && t < tiles; t += step) {
-                const int m0 = t / p.tiles_n * 256 + (int)rank * kARows;
-                const int n0 = t % p.tiles_n * p.BN + (int)rank * (p.BN / 2);
-                for (int s = 0; s < steps; ++s) {
-                    if (!mbar_wait(&tail->empty[st], phase ^ 1u, abort_flag, &g_err)) {
-                        ok = false;
-                        break;
-                    }
+        int st = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t full0 = map_rank(&tail->full[0], 0);
+        for (int t = first; ok && t < tiles; t += step) {
+            const int m0 = t / p.tiles_n * 256 + (int)rank * kARows;
+            const int n0 = t % p.tiles_n * p.BN + (int)rank * (p.BN / 2);
+            for (int s = 0; s < steps; ++s) {
+                if (!warp_wait(&tail->empty[st], phase ^ 1u, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                unsigned char* dst = smem + (size_t)st * stage_bytes;
+                const bool second = s >= p.steps0;
+                const int k = (second ? s - p.steps0 : s) * kBK;
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&tail->full[st], 2 * stage_bytes);
-                    const uint32_t bar = map_rank(&tail->full[st], 0);
-                    unsigned char* dst = smem + (size_t)st * stage_bytes;
-                    const bool second = s >= p.steps0;
-                    const int k = (second ? s - p.steps0 : s) * kBK;
-                    tma_load_2d_pair(dst, second ? &tmA1 : &tmA0, bar, k, m0);
-                    tma_load_2d_pair(dst + kABytes, second ? &tmW1 : &tmW0, bar, k, n0);
-                    if (++st == p.stages) {
-                        st = 0;
-                        phase ^= 1u;
-                    }
+                    tma_load_2d_pair(dst, second ? &tmA1 : &tmA0, full0 + 8u * (uint32_t)st, k, m0);
+                    tma_load_2d_pair(dst + kABytes, second ? &tmW1 : &tmW0, full0 + 8u * (uint32_t)st, k, n0);
+                }
+                __syncwarp();
+                if (++st == p.stages) {
+                    st = 0;
+                    phase ^= 1u;
                 }
             }
         }
     } else if (warp == 1) {
         // --------------------------------------------------------- MMA issuer
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
             const uint32_t idesc = idesc_bf16(256, p.BN);
             const uint64_t a_desc = smem_desc_kmajor(smem_u32(smem), 128);
             const uint64_t w_desc = smem_desc_kmajor(smem_u32(smem) + kABytes, 128);
@@ -206,27 +210,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int t = first; ok && t < tiles; t += step, ++it) {
                 const int b = it & 1;
-                if (!mbar_wait(&tail->acc_empty[b], ((it >> 1) & 1) ^ 1u, abort_flag, &g_err)) break;
+                if (!warp_wait(&tail->acc_empty[b], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)b * 256u;
                 for (int s = 0; s < steps; ++s) {
-                    if (!mbar_wait(&tail->full[st], phase, abort_flag, &g_err)) {
+                    if (!warp_wait(&tail->full[st], phase, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint64_t off = (uint64_t)(((uint32_t)st * stage_bytes) >> 4);
                     const int kn = s == p.steps0 - 1 ? last0 : (s == steps - 1 ? last1 : kBK / 16);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 16; ++kk)
-                        if (kk < kn) mma_bf16_pair(d, a_desc + off + 2 * kk, w_desc + off + 2 * kk, idesc, (s | kk) != 0);
-                    mma_commit_pair(&tail->empty[st]);
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            if (kk < kn) mma_bf16_pair(d, a_desc + off + 2 * kk, w_desc + off + 2 * kk, idesc, (s | kk) != 0);
+                        mma_commit_pair(&tail->empty[st]);
+                        if (s == steps - 1) mma_commit_pair(&tail->acc_full[b]);
+                    }
+                    __syncwarp();
                     if (++st == p.stages) {
                         st = 0;
                         phase ^= 1u;
                     }
                 }
-                if (ok) mma_commit_pair(&tail->acc_full[b]);
             }
         }
     } else if (warp >= 4) {

@@ -35,9 +35,38 @@ __device__ __forceinline__ float silu(float v) {
     return v / (1.0f + expf(-v));
 }
 
+// FAST GELU.  The tail q(a) = Phi(-a) = erfc(a / sqrt 2) / 2, a = |v|, is exp(-a^2 / 2) t P(t) with t = 1 / (1 + 0.3 a)
+// and P the degree-7 polynomial of least relative error (2^-23, a least-squares fit reweighted towards the
+// minimax one) to erfc(a / sqrt 2) exp(a^2 / 2) / (2t) on 0 <= a <= 13.2; beyond, q is below 2^-126 and v q rounds to
+// zero.  v Phi(v) is v q for negative v and v (1 - q) otherwise, so that the left tail keeps its relative error: with fp32
+// arithmetic below 2^-20, plus a^2 2^-24 through the exponential's argument.  Two values go through one reciprocal.
+__device__ __forceinline__ void gelu_pair(float& v0, float& v1) {
+    constexpr float P[8] = {0.1196245402097702f,  0.12082631886005402f, 0.09946505725383759f, 0.13003262877464294f,
+                            -0.056450121104717255f, 0.20934641361236572f, -0.15893374383449554f, 0.036088839173316956f};
+    const float a0 = fminf(fabsf(v0), 16.0f), a1 = fminf(fabsf(v1), 16.0f);   // (a NaN stays in the last product)
+    const uint64_t a = f2_pack(a0, a1);
+    float d0, d1, x0, x1;
+    f2_unpack(f2_fma(a, f2_pack(0.3f, 0.3f), f2_pack(1.0f, 1.0f)), d0, d1);
+    const float r = reciprocal(d0 * d1);
+    const uint64_t t = f2_pack(r * d1, r * d0);
+    uint64_t p = f2_pack(P[7], P[7]);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) p = f2_fma(p, t, f2_pack(P[i], P[i]));
+    f2_unpack(f2_mul(f2_mul(a, a), f2_pack(-0.72134752044448170f, -0.72134752044448170f)), x0, x1);   // -a^2 / 2 log2(e)
+    float q0, q1;
+    f2_unpack(f2_mul(f2_pack(exp2_fast(x0), exp2_fast(x1)), f2_mul(t, p)), q0, q1);
+    v0 *= v0 < 0.0f ? q0 : 1.0f - q0;
+    v1 *= v1 < 0.0f ? q1 : 1.0f - q1;
+}
+
 template <int ACT, bool FAST>
 __device__ __forceinline__ float activate(float v) {
     if (ACT == WINO_ACT_SILU) return silu<FAST>(v);
+    if (ACT == WINO_ACT_GELU && FAST) {
+        float other = 0.0f;
+        gelu_pair(v, other);
+        return v;
+    }
     if (ACT == WINO_ACT_GELU) return 0.5f * v * erfcf(v * -0.70710678118654752f);
     return v;
 }
@@ -83,6 +112,11 @@ __device__ __forceinline__ void activate_all(float (&v)[N]) {
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = w[i];
+        return;
+    }
+    if constexpr (ACT == WINO_ACT_GELU && FAST && N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) gelu_pair(v[i], v[i + 1]);
         return;
     }
 #pragma unroll

@@ -134,6 +134,19 @@ __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// True in one lane of a converged warp.  Loops that issue tensor-core or TMA instructions run in the whole warp, with
+// only the instruction itself under this predicate: their descriptors, coordinates and addresses are then the same in
+// all lanes and stay in uniform registers (inside `if (lane == 0)` each instruction first moves them there).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // The address of this CTA's shared variable in another CTA of the cluster.
 __device__ __forceinline__ uint32_t map_rank(const void* p, uint32_t rank) {
     uint32_t r;
