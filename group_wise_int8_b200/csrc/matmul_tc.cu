@@ -12,17 +12,17 @@
 //   rows per K step instead of 128 + BN: the L2-to-SM traffic of a lone CTA's
 //   128 x 256 tiles would exceed what the SMs' ports carry at the tensor
 //   cores' rate.
-//   warp 0    = TMA producer: 64 columns of K (128 bytes, 128-byte swizzle) of a
-//               or a2 and of w per stage; both CTAs' loads complete on the
+//   warp 0    = TMA producer: one or two blocks of 64 columns of K (128 bytes, 128-byte
+//               swizzle) of a or a2 and of w per stage; both CTAs' loads complete on the
 //               leader's barrier; columns past K read zeros.
 //   warp 1    = TMEM allocator; in the leader the MMA issuer; two accumulators of BN columns,
 //               so that the next tile's MMAs run under this tile's epilogue.
+//   warps 2, 3 = the chunk buffers of one epilogue group each: residual chunks in
+//               (TMA, up to four ahead), finished chunks out (TMA store).
 //   warps 4-11 = epilogue, two groups of four warps (the four TMEM lane
 //               quadrants) that take the tile's 32-column chunks in turn: fp32
 //               accumulator + bias, activation, + residual, rounded once into a chunk
-//               buffer (64- or 128-byte swizzle), stored by TMA.  The residual
-//               chunk has been loaded by TMA into that same buffer, up to three
-//               chunks ahead.
+//               buffer (64- or 128-byte swizzle) that holds the residual chunk.
 // Outputs or residuals whose base or pitch is no multiple of 16 bytes (an odd
 // number of columns) cannot go through TMA: there (DIRECT) each warp moves its own
 // 32 rows between the chunk buffer and memory, a row of 32 columns at a time.
@@ -51,7 +51,7 @@ constexpr size_t kSmemBudget = 226 * 1024;
 
 struct TcArgs {
     MatmulArgs m;
-    int BN, stages, tiles_m, tiles_n, steps0, steps1;
+    int BN, kb, stages, tiles_m, tiles_n, steps0, steps1;   // kb: K blocks of 64 per stage (1 or 2)
 };
 
 template <typename TO>
@@ -130,12 +130,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int NB = DIRECT ? 1 : Ch::kBuffers;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const uint32_t stage_bytes = kABytes + (uint32_t)(p.BN / 2) * kBK * 2;
+    const uint32_t block_bytes = kABytes + (uint32_t)(p.BN / 2) * kBK * 2;   // one K block of A, then of W
+    const uint32_t stage_bytes = (uint32_t)p.kb * block_bytes;
     unsigned char* chunks = smem + (size_t)p.stages * stage_bytes;   // [2 groups][NB][Ch::kBytes]
     Tail* tail = reinterpret_cast<Tail*>(chunks + 2 * NB * Ch::kBytes);
     volatile int* abort_flag = &tail->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    const uint32_t half = cluster_rank() & 1u;   // 0: the pair's leader, rows 0..127 of its tiles
+    const uint16_t mask = 3;
     const int tiles = p.tiles_m * p.tiles_n, step = (int)(gridDim.x / 2), first = (int)(blockIdx.x / 2);
     const int steps = p.steps0 + p.steps1;
     grid_dependents_launch();
@@ -161,12 +163,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!DIRECT) prefetch_tensormap(&tmOut);
     }
     if (warp == 1) tmem_alloc_pair(&tail->tmem_base, 512);
-    grid_dependency_wait();
     tc_fence_before();
     __syncthreads();
     cluster_sync();   // both CTAs' barriers exist before either signals the other's
     tc_fence_after();
+    grid_dependency_wait();   // (the setup above overlaps the previous kernel's tail)
     const uint32_t tmem_base = tail->tmem_base;
+    const bool has_res = p.m.res != nullptr;
+    auto origin_m = [&](int t) { return t / p.tiles_n * 256 + (int)half * kARows; };
+    auto origin_n = [&](int t, int c) { return t % p.tiles_n * p.BN + c * kChunk; };
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
@@ -175,20 +180,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bool ok = true;
         const uint32_t full0 = map_rank(&tail->full[0], 0);
         for (int t = first; ok && t < tiles; t += step) {
-            const int m0 = t / p.tiles_n * 256 + (int)rank * kARows;
-            const int n0 = t % p.tiles_n * p.BN + (int)rank * (p.BN / 2);
-            for (int s = 0; s < steps; ++s) {
+            const int m0 = t / p.tiles_n * 256 + (int)half * kARows;
+            const int n0 = t % p.tiles_n * p.BN + (int)half * (p.BN / 2);
+            for (int s = 0; s < steps; s += p.kb) {
                 if (!warp_wait(&tail->empty[st], phase ^ 1u, abort_flag)) {
                     ok = false;
                     break;
                 }
+                const uint32_t bar = full0 + 8u * (uint32_t)st;
                 unsigned char* dst = smem + (size_t)st * stage_bytes;
-                const bool second = s >= p.steps0;
-                const int k = (second ? s - p.steps0 : s) * kBK;
+                const int blocks = min(p.kb, steps - s);
                 if (elect_one()) {
-                    if (rank == 0) mbar_arrive_expect_tx(&tail->full[st], 2 * stage_bytes);
-                    tma_load_2d_pair(dst, second ? &tmA1 : &tmA0, full0 + 8u * (uint32_t)st, k, m0);
-                    tma_load_2d_pair(dst + kABytes, second ? &tmW1 : &tmW0, full0 + 8u * (uint32_t)st, k, n0);
+                    if (half == 0) mbar_arrive_expect_tx(&tail->full[st], 2u * (uint32_t)blocks * block_bytes);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (j < blocks) {
+                            const bool second = s + j >= p.steps0;
+                            const int k = (second ? s + j - p.steps0 : s + j) * kBK;
+                            tma_load_2d_pair(dst + j * block_bytes, second ? &tmA1 : &tmA0, bar, k, m0);
+                            tma_load_2d_pair(dst + j * block_bytes + kABytes, second ? &tmW1 : &tmW0, bar, k, n0);
+                        }
                 }
                 __syncwarp();
                 if (++st == p.stages) {
@@ -199,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // --------------------------------------------------------- MMA issuer
-        if (rank == 0) {
+        if (half == 0) {
             const uint32_t idesc = idesc_bf16(256, p.BN);
             const uint64_t a_desc = smem_desc_kmajor(smem_u32(smem), 128);
             const uint64_t w_desc = smem_desc_kmajor(smem_u32(smem) + kABytes, 128);
@@ -213,20 +224,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (!warp_wait(&tail->acc_empty[b], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag)) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)b * 256u;
-                for (int s = 0; s < steps; ++s) {
+                for (int s = 0; s < steps; s += p.kb) {
                     if (!warp_wait(&tail->full[st], phase, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t off = (uint64_t)(((uint32_t)st * stage_bytes) >> 4);
-                    const int kn = s == p.steps0 - 1 ? last0 : (s == steps - 1 ? last1 : kBK / 16);
+                    const uint32_t off = (uint32_t)st * (stage_bytes >> 4);
+                    const int blocks = min(p.kb, steps - s);
                     if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            if (kk < kn) mma_bf16_pair(d, a_desc + off + 2 * kk, w_desc + off + 2 * kk, idesc, (s | kk) != 0);
-                        mma_commit_pair(&tail->empty[st]);
-                        if (s == steps - 1) mma_commit_pair(&tail->acc_full[b]);
+                        for (int j = 0; j < 2; ++j)
+                            if (j < blocks) {
+                                const int kn = s + j == p.steps0 - 1 ? last0 : (s + j == steps - 1 ? last1 : kBK / 16);
+                                const uint64_t at = off + j * (block_bytes >> 4);
+#pragma unroll
+                                for (int kk = 0; kk < kBK / 16; ++kk)
+                                    if (kk < kn) mma_bf16_pair(d, a_desc + at + 2 * kk, w_desc + at + 2 * kk, idesc, (s | j | kk) != 0);
+                            }
+                        mma_commit_pair(&tail->empty[st], mask);
+                        if (s + p.kb >= steps) mma_commit_pair(&tail->acc_full[b], mask);
                     }
                     __syncwarp();
                     if (++st == p.stages) {
@@ -236,40 +253,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else if (warp < 4) {
+        // -------------------------------------- chunk buffers of one epilogue group
+        if constexpr (!DIRECT) {
+            const int g = warp - 2;
+            unsigned char* ring = chunks + (size_t)g * NB * Ch::kBytes;
+            Cursor cur{first, g, step, tiles, p.tiles_n, p.BN, p.m.N, g};
+            cur.settle();
+            Cursor ahead = cur;
+            auto hand_out = [&](int buf) {   // a free buffer, for the chunk at `ahead`
+                if (!has_res) {
+                    mbar_arrive(&tail->buf_full[g][buf]);
+                } else if (ahead.valid()) {
+                    mbar_arrive_expect_tx(&tail->buf_full[g][buf], Ch::kBytes);
+                    tma_load_2d(ring + buf * Ch::kBytes, &tmRes, &tail->buf_full[g][buf], origin_n(ahead.tile, ahead.c),
+                                origin_m(ahead.tile));
+                    ahead.next();
+                }
+            };
+            if (lane == 0)
+                for (int i = 0; i < NB; ++i) hand_out(i);
+            __syncwarp();
+            int buf = 0;
+            uint32_t phase = 0;
+            for (int i = 0; cur.valid(); cur.next(), ++i) {
+                if (!warp_wait(&tail->buf_ready[g][buf], phase, abort_flag)) break;
+                if (lane == 0) {
+                    const int m0 = origin_m(cur.tile);
+                    if (m0 < p.m.M) tma_store_2d(&tmOut, ring + buf * Ch::kBytes, origin_n(cur.tile, cur.c), m0);
+                    bulk_commit();
+                    bulk_wait_read<1>();   // the store before this one has read its buffer, which is handed out again
+                    if (i > 0) hand_out((buf + NB - 1) % NB);
+                }
+                __syncwarp();
+                if (++buf == NB) {
+                    buf = 0;
+                    phase ^= 1u;
+                }
+            }
+            if (lane == 0) bulk_wait_read<0>();
+        }
+    } else {
         // ----------------------------------------------------------- epilogue
         const int g = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
         const uint32_t t_lane = tmem_base + ((uint32_t)(32 * quad) << 16);
         unsigned char* ring = chunks + (size_t)g * NB * Ch::kBytes;
         float* bias_s = tail->bias[warp - 4];
         const uint32_t release = map_rank(&tail->acc_empty[0], 0);
-        const bool chief = quad == 0 && lane == 0;   // issues the group's TMA operations
-        const bool has_res = p.m.res != nullptr;
-        auto origin_m = [&](int t) { return t / p.tiles_n * 256 + (int)rank * kARows; };
-        auto origin_n = [&](int t, int c) { return t % p.tiles_n * p.BN + c * kChunk; };
-        Cursor cur{first, g, step, tiles, p.tiles_n, p.BN, p.m.N, g};
-        Cursor ahead = cur;
-        ahead.settle();
-        auto hand_out = [&](int buf) {   // a free buffer, for the chunk at `ahead`
-            if (!has_res) {
-                mbar_arrive(&tail->buf_full[g][buf]);
-            } else if (ahead.valid()) {
-                mbar_arrive_expect_tx(&tail->buf_full[g][buf], Ch::kBytes);
-                tma_load_2d(ring + buf * Ch::kBytes, &tmRes, &tail->buf_full[g][buf], origin_n(ahead.tile, ahead.c),
-                            origin_m(ahead.tile));
-                ahead.next();
-            }
-        };
-        if (!DIRECT && chief)
-            for (int i = 0; i < NB - 1; ++i) hand_out(i);
-
         int it = 0, buf = 0;
         uint32_t rphase = 0;
         bool ok = true;
         for (int t = first; ok && t < tiles; t += step, ++it) {
             const int b = it & 1;
-            cur.tile = t;
-            const int nch = cur.chunks(), m0 = origin_m(t);
+            const int nch = (min(p.BN, p.m.N - origin_n(t, 0)) + kChunk - 1) / kChunk, m0 = origin_m(t);
+            auto bias_of = [&](int c) {   // this lane's column of chunk c
+                const int n = origin_n(t, c) + lane;
+                return p.m.bias && c < nch && n < p.m.N ? p.m.bias[n] : 0.0f;
+            };
+            float bias_next = bias_of(g);   // on its way before the accumulator is complete
             if (!warp_wait(&tail->acc_full[b], (uint32_t)((it >> 1) & 1), abort_flag)) break;
             tc_fence_after();
             for (int c = g; c < nch; c += 2) {
@@ -277,7 +318,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 unsigned char* cb = ring + (size_t)buf * Ch::kBytes;
                 uint32_t r[kChunk];
                 tmem_ld<kChunk>(t_lane + (uint32_t)(b * 256 + c * kChunk), r);
-                bias_s[lane] = p.m.bias && n0 + lane < p.m.N ? p.m.bias[n0 + lane] : 0.0f;
+                bias_s[lane] = bias_next;
+                bias_next = bias_of(c + 2);
                 if (DIRECT && has_res) {
                     const TO* res = static_cast<const TO*>(p.m.res);
                     const int rows = min(32, p.m.M - m0 - 32 * quad);
@@ -360,19 +402,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&tail->buf_ready[g][buf]);
-                    if (quad == 0) {
-                        if (!warp_wait(&tail->buf_ready[g][buf], rphase, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        if (lane == 0) {
-                            if (m0 < p.m.M) tma_store_2d(&tmOut, cb, n0, m0);
-                            bulk_commit();
-                            bulk_wait_read<1>();   // the store before this one has read its buffer, which is handed out again
-                            hand_out((buf + NB - 1) % NB);
-                        }
-                        __syncwarp();
-                    }
                     if (++buf == NB) {
                         buf = 0;
                         rphase ^= 1u;
@@ -384,7 +413,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
             }
         }
-        if (!DIRECT && chief) bulk_wait_read<0>();
     }
 
     // Every role is done: the MMAs that read either CTA's shared memory have completed (both epilogues waited
@@ -401,7 +429,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 size_t smem_bytes(const TcArgs& a, bool direct) {
     const size_t chunk = a.m.out_bf16 ? Chunk<__nv_bfloat16>::kBytes : Chunk<float>::kBytes;
     const size_t buffers = direct ? 1 : (a.m.out_bf16 ? Chunk<__nv_bfloat16>::kBuffers : Chunk<float>::kBuffers);
-    return 1024 + (size_t)a.stages * (kABytes + a.BN / 2 * kBK * 2) + 2 * buffers * chunk + sizeof(Tail);
+    return 1024 + (size_t)a.stages * a.kb * (kABytes + a.BN / 2 * kBK * 2) + 2 * buffers * chunk + sizeof(Tail);
 }
 
 bool tma_ok(const void* p, long pitch, int rows, size_t es) {
@@ -473,6 +501,9 @@ cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStrea
         if (!map_2d(&out, m.out_bf16, m.out, m.N, m.M, m.ldo, kChunk, kARows)) return cudaErrorInvalidValue;
         if (m.res && !map_2d(&res, m.out_bf16, m.res, m.N, m.M, m.ldr, kChunk, kARows)) return cudaErrorInvalidValue;
     }
+    // two K blocks per stage where their MMAs take less time than the issue loops' turn (about 340 cycles; a block
+    // takes 2 BN), as long as three stages fit
+    a.kb = a.BN <= 160 ? 2 : 1;
     a.stages = kMaxStages;
     while (a.stages > 2 && smem_bytes(a, direct) > kSmemBudget) --a.stages;
     const size_t smem = smem_bytes(a, direct);

@@ -223,12 +223,13 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrives (once) on the same barrier of both CTAs of a pair when all prior pair MMAs of this thread complete.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// Arrives (once) on the same barrier of both CTAs of a pair (mask: their cluster ranks) when all prior pair MMAs of
+// this thread complete.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"(mask)
         : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
