@@ -20,7 +20,7 @@
 //   warps 2, 3 = the chunk buffers of one epilogue group each: residual chunks in
 //               (TMA, up to four ahead), finished chunks out (TMA store).
 //   warps 4-11 = epilogue, two groups of four warps (the four TMEM lane
-//               quadrants) that take the tile's 32-column chunks in turn: fp32
+//               quadrants) that take the tile's 64-column (fp32 output: 32) chunks in turn: fp32
 //               accumulator + bias, activation, + residual, rounded once into a chunk
 //               buffer (64- or 128-byte swizzle) that holds the residual chunk.
 // Outputs or residuals whose base or pitch is no multiple of 16 bytes (an odd
@@ -28,6 +28,7 @@
 // 32 rows between the chunk buffer and memory, a row of 32 columns at a time.
 // Every mbarrier wait is bounded; on expiry the CTA records the error and leaves.
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -44,7 +45,6 @@ __device__ int g_err;   // first error since matmul_tc_take_error
 constexpr int kThreads = 384;
 constexpr int kBK = 64;               // K per stage
 constexpr int kMaxStages = 8;
-constexpr int kChunk = 32;            // columns per epilogue chunk
 constexpr int kARows = 128;           // rows of A per CTA
 constexpr uint32_t kABytes = kARows * kBK * 2;
 constexpr size_t kSmemBudget = 226 * 1024;
@@ -54,29 +54,28 @@ struct TcArgs {
     int BN, kb, stages, tiles_m, tiles_n, steps0, steps1;   // kb: K blocks of 64 per stage (1 or 2)
 };
 
-template <typename TO>
+// Epilogue chunks: 128 rows of 128 bytes (64 bf16 or 32 fp32 columns) in the 128-byte swizzle; where a tile's width
+// leaves half a bf16 chunk, and in the DIRECT kernels, 32 columns.
+template <typename TO, bool DIRECT>
 struct Chunk {
-    static constexpr int kRow = kChunk * (int)sizeof(TO);     // bytes of a row: 64 or 128, the swizzle's width
-    static constexpr int kBytes = kARows * kRow;
-    static constexpr int kBuffers = sizeof(TO) == 2 ? 4 : 2;  // per epilogue group
-    // byte offset of 16-byte unit j of a row (the TMA swizzle of that width)
-    static __device__ __forceinline__ uint32_t unit(int row, int j) {
-        return (uint32_t)(row * kRow + ((j ^ (sizeof(TO) == 2 ? (row >> 1) & 3 : row & 7)) << 4));
-    }
-    static __device__ __forceinline__ uint32_t at(int row, int col) {
-        constexpr int per = 16 / (int)sizeof(TO);
-        return unit(row, col / per) + (uint32_t)(col % per * (int)sizeof(TO));
-    }
+    static constexpr int kCols = DIRECT ? 32 : 128 / (int)sizeof(TO);
+    static constexpr int kBytes = kARows * kCols * (int)sizeof(TO);
+    static constexpr int kBuffers = DIRECT ? 1 : 2;   // per epilogue group
 };
+// Byte offset of 16-byte unit j of a row of ROW bytes (64 or 128: the TMA swizzle of that width).
+template <int ROW>
+__device__ __forceinline__ uint32_t chunk_unit(int row, int j) {
+    return (uint32_t)(row * ROW + ((j ^ (ROW == 64 ? (row >> 1) & 3 : row & 7)) << 4));
+}
 
 struct Tail {
     uint64_t full[kMaxStages];     // leader: both CTAs' operands of the stage have landed
     uint64_t empty[kMaxStages];    // the pair's MMAs have read the stage
     uint64_t acc_full[2];
     uint64_t acc_empty[2];         // leader: both CTAs' epilogues have read the accumulator
-    uint64_t buf_full[2][4];       // a group's chunk buffer is free to use, its residual (if any) landed
-    uint64_t buf_ready[2][4];      // ... and holds the output chunk: the group's four warps have written it
-    alignas(16) float bias[8][kChunk];   // per epilogue warp
+    uint64_t buf_full[2][2];       // a group's chunk buffer is free to use, its residual (if any) landed
+    uint64_t buf_ready[2][2];      // ... and holds the output chunk: the group's four warps have written it
+    alignas(16) float bias[8][64];   // per epilogue warp
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -101,23 +100,52 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
-// The chunks of one epilogue group, tile after tile: chunk c of tile t, c = g, g + 2, ...
-struct Cursor {
-    int tile, c, step, tiles, tiles_n, BN, N, g;
-    __device__ __forceinline__ int chunks() const {   // of the tile
-        const int n0 = tile % tiles_n * BN;
-        return (min(BN, N - n0) + kChunk - 1) / kChunk;
+// A pair's tiles, in steps of the grid's pairs (no division on the way).
+struct Tile {
+    int t, m, n;             // index, row of tiles, column of tiles
+    int step, step_m, step_n;
+    __device__ __forceinline__ Tile(const TcArgs& p, int first, int grid_pairs) {
+        t = first;
+        m = first / p.tiles_n;
+        n = first - m * p.tiles_n;
+        step = grid_pairs;
+        step_m = step / p.tiles_n;
+        step_n = step - step_m * p.tiles_n;
     }
-    __device__ __forceinline__ bool valid() const { return tile < tiles; }
-    __device__ __forceinline__ void settle() {        // to the next existing chunk
-        while (tile < tiles && c >= chunks()) {
-            tile += step;
+    __device__ __forceinline__ void next(const TcArgs& p) {
+        t += step;
+        m += step_m;
+        n += step_n;
+        if (n >= p.tiles_n) {
+            n -= p.tiles_n;
+            ++m;
+        }
+    }
+    __device__ __forceinline__ bool valid(const TcArgs& p) const { return t < p.tiles_m * p.tiles_n; }
+};
+
+// Chunks of COLS columns in a tile.
+template <int COLS>
+__device__ __forceinline__ int chunks_of(const TcArgs& p, const Tile& t) {
+    return (min(p.BN, p.m.N - t.n * p.BN) + COLS - 1) / COLS;
+}
+
+// The chunks of one epilogue group, tile after tile: chunk c of each tile, c = g, g + 2, ...
+template <int COLS>
+struct Cursor {
+    Tile tile;
+    int c, g;
+    __device__ __forceinline__ Cursor(const Tile& first, int group, const TcArgs& p) : tile(first), c(group), g(group) { settle(p); }
+    __device__ __forceinline__ bool valid(const TcArgs& p) const { return tile.valid(p); }
+    __device__ __forceinline__ void settle(const TcArgs& p) {   // to the next existing chunk
+        while (tile.valid(p) && c >= chunks_of<COLS>(p, tile)) {
+            tile.next(p);
             c = g;
         }
     }
-    __device__ __forceinline__ void next() {
+    __device__ __forceinline__ void next(const TcArgs& p) {
         c += 2;
-        settle();
+        settle(p);
     }
 };
 
@@ -125,9 +153,11 @@ template <typename TO, bool DIRECT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                      const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
-                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes, const TcArgs p) {
-    using Ch = Chunk<TO>;
-    constexpr int NB = DIRECT ? 1 : Ch::kBuffers;
+                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes,
+                     const __grid_constant__ CUtensorMap tmOutHalf, const __grid_constant__ CUtensorMap tmResHalf,
+                     const TcArgs p) {
+    using Ch = Chunk<TO, DIRECT>;
+    constexpr int NB = Ch::kBuffers, CW = Ch::kCols;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t block_bytes = kABytes + (uint32_t)(p.BN / 2) * kBK * 2;   // one K block of A, then of W
@@ -138,7 +168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t half = cluster_rank() & 1u;   // 0: the pair's leader, rows 0..127 of its tiles
     const uint16_t mask = 3;
-    const int tiles = p.tiles_m * p.tiles_n, step = (int)(gridDim.x / 2), first = (int)(blockIdx.x / 2);
+    const Tile first(p, (int)(blockIdx.x / 2), (int)(gridDim.x / 2));
     const int steps = p.steps0 + p.steps1;
     grid_dependents_launch();
 
@@ -170,8 +200,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     grid_dependency_wait();   // (the setup above overlaps the previous kernel's tail)
     const uint32_t tmem_base = tail->tmem_base;
     const bool has_res = p.m.res != nullptr;
-    auto origin_m = [&](int t) { return t / p.tiles_n * 256 + (int)half * kARows; };
-    auto origin_n = [&](int t, int c) { return t % p.tiles_n * p.BN + c * kChunk; };
+    auto origin_m = [&](const Tile& t) { return t.m * 256 + (int)half * kARows; };
+    auto origin_n = [&](const Tile& t, int c) { return t.n * p.BN + c * CW; };
+    auto half_chunk = [&](int c) { return CW == 64 && c * CW + CW > p.BN; };   // the tile ends in its middle
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
@@ -179,9 +210,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t phase = 0;
         bool ok = true;
         const uint32_t full0 = map_rank(&tail->full[0], 0);
-        for (int t = first; ok && t < tiles; t += step) {
-            const int m0 = t / p.tiles_n * 256 + (int)half * kARows;
-            const int n0 = t % p.tiles_n * p.BN + (int)half * (p.BN / 2);
+        for (Tile t = first; ok && t.valid(p); t.next(p)) {
+            const int m0 = origin_m(t), n0 = t.n * p.BN + (int)half * (p.BN / 2);
             for (int s = 0; s < steps; s += p.kb) {
                 if (!warp_wait(&tail->empty[st], phase ^ 1u, abort_flag)) {
                     ok = false;
@@ -219,7 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int st = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = first; ok && t < tiles; t += step, ++it) {
+            for (Tile t = first; ok && t.valid(p); t.next(p), ++it) {
                 const int b = it & 1;
                 if (!warp_wait(&tail->acc_empty[b], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag)) break;
                 tc_fence_after();
@@ -258,17 +288,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if constexpr (!DIRECT) {
             const int g = warp - 2;
             unsigned char* ring = chunks + (size_t)g * NB * Ch::kBytes;
-            Cursor cur{first, g, step, tiles, p.tiles_n, p.BN, p.m.N, g};
-            cur.settle();
-            Cursor ahead = cur;
+            Cursor<CW> cur(first, g, p), ahead = cur;
             auto hand_out = [&](int buf) {   // a free buffer, for the chunk at `ahead`
                 if (!has_res) {
                     mbar_arrive(&tail->buf_full[g][buf]);
-                } else if (ahead.valid()) {
-                    mbar_arrive_expect_tx(&tail->buf_full[g][buf], Ch::kBytes);
-                    tma_load_2d(ring + buf * Ch::kBytes, &tmRes, &tail->buf_full[g][buf], origin_n(ahead.tile, ahead.c),
-                                origin_m(ahead.tile));
-                    ahead.next();
+                } else if (ahead.valid(p)) {
+                    const bool hc = half_chunk(ahead.c);
+                    mbar_arrive_expect_tx(&tail->buf_full[g][buf], hc ? Ch::kBytes / 2 : Ch::kBytes);
+                    tma_load_2d(ring + buf * Ch::kBytes, hc ? &tmResHalf : &tmRes, &tail->buf_full[g][buf],
+                                origin_n(ahead.tile, ahead.c), origin_m(ahead.tile));
+                    ahead.next(p);
                 }
             };
             if (lane == 0)
@@ -276,11 +305,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             int buf = 0;
             uint32_t phase = 0;
-            for (int i = 0; cur.valid(); cur.next(), ++i) {
+            for (int i = 0; cur.valid(p); cur.next(p), ++i) {
                 if (!warp_wait(&tail->buf_ready[g][buf], phase, abort_flag)) break;
                 if (lane == 0) {
                     const int m0 = origin_m(cur.tile);
-                    if (m0 < p.m.M) tma_store_2d(&tmOut, ring + buf * Ch::kBytes, origin_n(cur.tile, cur.c), m0);
+                    if (m0 < p.m.M)
+                        tma_store_2d(half_chunk(cur.c) ? &tmOutHalf : &tmOut, ring + buf * Ch::kBytes, origin_n(cur.tile, cur.c), m0);
                     bulk_commit();
                     bulk_wait_read<1>();   // the store before this one has read its buffer, which is handed out again
                     if (i > 0) hand_out((buf + NB - 1) % NB);
@@ -303,112 +333,129 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int it = 0, buf = 0;
         uint32_t rphase = 0;
         bool ok = true;
-        for (int t = first; ok && t < tiles; t += step, ++it) {
-            const int b = it & 1;
-            const int nch = (min(p.BN, p.m.N - origin_n(t, 0)) + kChunk - 1) / kChunk, m0 = origin_m(t);
-            auto bias_of = [&](int c) {   // this lane's column of chunk c
-                const int n = origin_n(t, c) + lane;
-                return p.m.bias && c < nch && n < p.m.N ? p.m.bias[n] : 0.0f;
-            };
-            float bias_next = bias_of(g);   // on its way before the accumulator is complete
-            if (!warp_wait(&tail->acc_full[b], (uint32_t)((it >> 1) & 1), abort_flag)) break;
-            tc_fence_after();
-            for (int c = g; c < nch; c += 2) {
-                const int n0 = origin_n(t, c);
-                unsigned char* cb = ring + (size_t)buf * Ch::kBytes;
-                uint32_t r[kChunk];
-                tmem_ld<kChunk>(t_lane + (uint32_t)(b * 256 + c * kChunk), r);
-                bias_s[lane] = bias_next;
-                bias_next = bias_of(c + 2);
-                if (DIRECT && has_res) {
-                    const TO* res = static_cast<const TO*>(p.m.res);
-                    const int rows = min(32, p.m.M - m0 - 32 * quad);
-                    if (n0 + lane < p.m.N)
+        // One chunk of W columns at column n0 of the output, from TMEM column `tcol`; `last`: this warp's last read of
+        // accumulator b.
+        auto chunk = [&](auto width, int n0, int m0, uint32_t tcol, int b, bool last) {
+            constexpr int W = decltype(width)::value, ROW = W * (int)sizeof(TO), PER = 16 / (int)sizeof(TO);
+            unsigned char* cb = ring + (size_t)buf * Ch::kBytes;
+            uint32_t r[W];
+#pragma unroll
+            for (int j = 0; j < W; j += 32) tmem_ld<32>(t_lane + tcol + (uint32_t)j, *reinterpret_cast<uint32_t(*)[32]>(r + j));
+            if (DIRECT && has_res) {
+                const TO* res = static_cast<const TO*>(p.m.res);
+                const int rows = min(32, p.m.M - m0 - 32 * quad);
+                if (n0 + lane < p.m.N)
 #pragma unroll 8
-                        for (int i = 0; i < rows; ++i)
-                            *reinterpret_cast<TO*>(cb + Ch::at(32 * quad + i, lane)) =
-                                res[(size_t)(m0 + 32 * quad + i) * p.m.ldr + n0 + lane];
-                }
+                    for (int i = 0; i < rows; ++i)
+                        *reinterpret_cast<TO*>(cb + chunk_unit<ROW>(32 * quad + i, lane / PER) + lane % PER * sizeof(TO)) =
+                            res[(size_t)(m0 + 32 * quad + i) * p.m.ldr + n0 + lane];
+            }
+            __syncwarp();
+            tmem_ld_wait();
+            tmem_regs_ready(r);
+            if (last) {
+                tc_fence_before();
                 __syncwarp();
-                tmem_ld_wait();
-                tmem_regs_ready(r);
-                if (c + 2 >= nch) {   // this warp's last read of the accumulator
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
-                }
-                float v[kChunk];
+                if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
+            }
+            float v[W];
 #pragma unroll
-                for (int j = 0; j < kChunk; j += 4) {
-                    const float4 bb = *reinterpret_cast<const float4*>(bias_s + j);
-                    v[j] = __uint_as_float(r[j]) + bb.x;
-                    v[j + 1] = __uint_as_float(r[j + 1]) + bb.y;
-                    v[j + 2] = __uint_as_float(r[j + 2]) + bb.z;
-                    v[j + 3] = __uint_as_float(r[j + 3]) + bb.w;
-                }
-                if (p.m.act == WINO_ACT_SILU) activate_all<WINO_ACT_SILU, sizeof(TO) == 2>(v);
-                if (p.m.act == WINO_ACT_GELU) activate_all<WINO_ACT_GELU, sizeof(TO) == 2>(v);
-                if (!DIRECT && !warp_wait(&tail->buf_full[g][buf], rphase, abort_flag)) {
-                    ok = false;
-                    break;
-                }
-                if (has_res) {
+            for (int j = 0; j < W; j += 4) {
+                const float4 bb = *reinterpret_cast<const float4*>(bias_s + j);
+                v[j] = __uint_as_float(r[j]) + bb.x;
+                v[j + 1] = __uint_as_float(r[j + 1]) + bb.y;
+                v[j + 2] = __uint_as_float(r[j + 2]) + bb.z;
+                v[j + 3] = __uint_as_float(r[j + 3]) + bb.w;
+            }
+            if (p.m.act == WINO_ACT_SILU) activate_all<WINO_ACT_SILU, sizeof(TO) == 2>(v);
+            if (p.m.act == WINO_ACT_GELU) activate_all<WINO_ACT_GELU, sizeof(TO) == 2>(v);
+            if (!DIRECT && !warp_wait(&tail->buf_full[g][buf], rphase, abort_flag)) {
+                ok = false;
+                return;
+            }
+            if (has_res) {
 #pragma unroll
-                    for (int j = 0; j < Ch::kRow / 16; ++j) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(cb + Ch::unit(row, j));
-                        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                for (int j = 0; j < ROW / 16; ++j) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(cb + chunk_unit<ROW>(row, j));
+                    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if constexpr (sizeof(TO) == 2) {
-                                v[8 * j + 2 * i] += __uint_as_float(x[i] << 16);
-                                v[8 * j + 2 * i + 1] += __uint_as_float(x[i] & 0xffff0000u);
-                            } else {
-                                v[4 * j + i] += __uint_as_float(x[i]);
-                            }
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (sizeof(TO) == 2) {
+                            v[8 * j + 2 * i] += __uint_as_float(x[i] << 16);
+                            v[8 * j + 2 * i + 1] += __uint_as_float(x[i] & 0xffff0000u);
+                        } else {
+                            v[4 * j + i] += __uint_as_float(x[i]);
                         }
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < Ch::kRow / 16; ++j) {
-                    uint4 w;
-                    if constexpr (sizeof(TO) == 2) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
-                            x[i] = *reinterpret_cast<const uint32_t*>(&h);
-                        }
-                        w = make_uint4(x[0], x[1], x[2], x[3]);
-                    } else {
-                        w = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
-                                       __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
-                    }
-                    *reinterpret_cast<uint4*>(cb + Ch::unit(row, j)) = w;
-                }
-                if constexpr (DIRECT) {
-                    __syncwarp();
-                    TO* out = static_cast<TO*>(p.m.out);
-                    const int rows = min(32, p.m.M - m0 - 32 * quad);
-                    const size_t limit = (size_t)(p.m.M - 1) * p.m.ldo + p.m.N;
-                    if (n0 + lane < p.m.N)
-#pragma unroll 8
-                        for (int i = 0; i < rows; ++i) {
-                            const size_t at = (size_t)(m0 + 32 * quad + i) * p.m.ldo + n0 + lane;
-                            if (in_bounds(at, limit, &g_err))
-                                out[at] = *reinterpret_cast<const TO*>(cb + Ch::at(32 * quad + i, lane));
-                        }
-                    __syncwarp();
-                } else {
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&tail->buf_ready[g][buf]);
-                    if (++buf == NB) {
-                        buf = 0;
-                        rphase ^= 1u;
                     }
                 }
             }
+#pragma unroll
+            for (int j = 0; j < ROW / 16; ++j) {
+                uint4 w;
+                if constexpr (sizeof(TO) == 2) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+                        x[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    w = make_uint4(x[0], x[1], x[2], x[3]);
+                } else {
+                    w = make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]),
+                                   __float_as_uint(v[4 * j + 3]));
+                }
+                *reinterpret_cast<uint4*>(cb + chunk_unit<ROW>(row, j)) = w;
+            }
+            if constexpr (DIRECT) {
+                __syncwarp();
+                TO* out = static_cast<TO*>(p.m.out);
+                const int rows = min(32, p.m.M - m0 - 32 * quad);
+                const size_t limit = (size_t)(p.m.M - 1) * p.m.ldo + p.m.N;
+                if (n0 + lane < p.m.N)
+#pragma unroll 8
+                    for (int i = 0; i < rows; ++i) {
+                        const size_t at = (size_t)(m0 + 32 * quad + i) * p.m.ldo + n0 + lane;
+                        if (in_bounds(at, limit, &g_err))
+                            out[at] = *reinterpret_cast<const TO*>(cb + chunk_unit<ROW>(32 * quad + i, lane / PER) + lane % PER * sizeof(TO));
+                    }
+            } else {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tail->buf_ready[g][buf]);
+                if (++buf == NB) {
+                    buf = 0;
+                    rphase ^= 1u;
+                }
+            }
+            __syncwarp();
+        };
+        float bias_next[CW / 32];   // this lane's columns of the next chunk, on their way before it starts
+        auto fetch_bias = [&](const Tile& t, int c) {
+#pragma unroll
+            for (int j = 0; j < CW / 32; ++j) {
+                const int n = origin_n(t, c) + 32 * j + lane;
+                bias_next[j] = p.m.bias && n < p.m.N ? p.m.bias[n] : 0.0f;
+            }
+        };
+        fetch_bias(first, g);
+        Tile following = first;
+        for (Tile t = first; ok && t.valid(p); t = following, ++it) {
+            const int b = it & 1;
+            const int nch = chunks_of<CW>(p, t), m0 = origin_m(t);
+            following.next(p);
+            if (!warp_wait(&tail->acc_full[b], (uint32_t)((it >> 1) & 1), abort_flag)) break;
+            tc_fence_after();
+            for (int c = g; ok && c < nch; c += 2) {
+#pragma unroll
+                for (int j = 0; j < CW / 32; ++j) bias_s[32 * j + lane] = bias_next[j];
+                if (c + 2 < nch) fetch_bias(t, c + 2);
+                else fetch_bias(following, g);
+                const uint32_t tcol = (uint32_t)(b * 256 + c * CW);
+                if (half_chunk(c)) chunk(std::integral_constant<int, 32>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch);
+                else chunk(std::integral_constant<int, CW>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch);
+            }
             if (g >= nch) {   // a tile of one chunk leaves the second group nothing to read
+                fetch_bias(following, g);
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
             }
@@ -427,9 +474,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 size_t smem_bytes(const TcArgs& a, bool direct) {
-    const size_t chunk = a.m.out_bf16 ? Chunk<__nv_bfloat16>::kBytes : Chunk<float>::kBytes;
-    const size_t buffers = direct ? 1 : (a.m.out_bf16 ? Chunk<__nv_bfloat16>::kBuffers : Chunk<float>::kBuffers);
-    return 1024 + (size_t)a.stages * a.kb * (kABytes + a.BN / 2 * kBK * 2) + 2 * buffers * chunk + sizeof(Tail);
+    const size_t chunks = direct ? (a.m.out_bf16 ? Chunk<__nv_bfloat16, true>::kBytes : Chunk<float, true>::kBytes)
+                                 : (size_t)Chunk<float, false>::kBuffers * Chunk<float, false>::kBytes;   // (either type)
+    return 1024 + (size_t)a.stages * a.kb * (kABytes + a.BN / 2 * kBK * 2) + 2 * chunks + sizeof(Tail);
 }
 
 bool tma_ok(const void* p, long pitch, int rows, size_t es) {
@@ -494,12 +541,18 @@ cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStrea
     a.steps1 = (m.K1 + kBK - 1) / kBK;
     const size_t so = m.out_bf16 ? 2 : 4;
     const bool direct = !tma_ok(m.out, m.ldo, m.M, so) || (m.res && !tma_ok(m.res, m.ldr, m.M, so));
-    CUtensorMap map[4], out, res;
+    CUtensorMap map[4], out, res, out_half, res_half;
     if (!matmul_operand_maps(m, a.BN / 2, map)) return cudaErrorInvalidValue;
-    out = res = map[0];
+    out = res = out_half = res_half = map[0];
     if (!direct) {
-        if (!map_2d(&out, m.out_bf16, m.out, m.N, m.M, m.ldo, kChunk, kARows)) return cudaErrorInvalidValue;
-        if (m.res && !map_2d(&res, m.out_bf16, m.res, m.N, m.M, m.ldr, kChunk, kARows)) return cudaErrorInvalidValue;
+        const int cols = 128 / (int)so;
+        bool ok = map_2d(&out, m.out_bf16, m.out, m.N, m.M, m.ldo, cols, kARows);
+        if (m.res) ok = ok && map_2d(&res, m.out_bf16, m.res, m.N, m.M, m.ldr, cols, kARows);
+        if (m.out_bf16 && a.BN % 64 != 0) {
+            ok = ok && map_2d(&out_half, true, m.out, m.N, m.M, m.ldo, 32, kARows);
+            if (m.res) ok = ok && map_2d(&res_half, true, m.res, m.N, m.M, m.ldr, 32, kARows);
+        }
+        if (!ok) return cudaErrorInvalidValue;
     }
     // two K blocks per stage where their MMAs take less time than the issue loops' turn (about 340 cycles; a block
     // takes 2 BN), as long as three stages fit
@@ -513,7 +566,7 @@ cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStrea
         const cudaError_t e = allow_smem(kern, kSmemBudget, d);
         if (e != cudaSuccess) return e;
         return launch_dependent(kern, dim3((unsigned)(2 * pairs)), dim3(kThreads), smem, st, map[0], map[1], map[2], map[3],
-                                out, res, a);
+                                out, res, out_half, res_half, a);
     };
     if (m.out_bf16)
         return direct ? go(matmul_tc_kernel<__nv_bfloat16, true>, done[0]) : go(matmul_tc_kernel<__nv_bfloat16, false>, done[1]);
