@@ -26,7 +26,7 @@ LIB = os.path.join(HERE, "libwino_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libwino_b200_debug.so")
 SOURCES = ["plan.cpp", "api.cu", "weight_transform.cu", "input_transform.cu", "hadamard_tc.cu",
            "hadamard_simt.cu", "output_transform.cu", "input_quant.cu", "noalloc.cu", "fused_small.cu",
-           "ops_api.cu", "group_norm.cu", "matmul_simt.cu", "matmul_tc.cu"]
+           "ops_api.cu", "group_norm.cu", "matmul_simt.cu", "matmul_rows.cu", "matmul_tc.cu"]
 HEADERS = ["plan.h", "common.cuh", "sm100.cuh", "kernels.h", "ops.h"]
 TORCH_OPS = os.path.join(HERE, "torch_ops_b200.so")   # torch marshalling of the operators beside the convolution
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -91,7 +91,7 @@ def _build_torch_ops(src: str) -> None:
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = TORCH_OPS + ".tmp%d" % os.getpid()
     cmd = ["g++", "-shared", "-std=c++17", "-O2", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
-           *["-isystem" + i for i in inc], src, "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           *["-isystem" + i for i in inc], src, "-o", tmp, "-L" + lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("g++ failed for torch_ops.cpp:\n%s\n%s" % (r.stdout, r.stderr))

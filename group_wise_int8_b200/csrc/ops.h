@@ -71,47 +71,34 @@ __device__ __forceinline__ float activate(float v) {
     return v;
 }
 
-// min of three, NaN if one is NaN.
-__device__ __forceinline__ float min3_nan(float a, float b, float c) {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
+// FAST SiLU of four values with one reciprocal, since the special-function unit is its bound (1.25 operations there per
+// value instead of 2).  With e = exp(-|v|) and d = 1 + e, at most 2, v sigmoid(v) is v / d for v >= 0 and v e / d
+// otherwise; X = (d0 d2, d1 d3) and r = 1 / (X0 X1) give the reciprocals of (d0, d1) as (r X1, r X0) (d2, d3) and those of
+// (d2, d3) as the same pair times (d0, d1).  (min drops a NaN, which would reach its neighbours through r; the last
+// product restores it.)
+__device__ __forceinline__ void silu_quad(float& v0, float& v1, float& v2, float& v3) {
+    const uint64_t scale = f2_pack(-1.4426950408889634f, -1.4426950408889634f), one = f2_pack(1.0f, 1.0f);
+    float t0, t1, t2, t3, x0, x1;
+    f2_unpack(f2_mul(f2_pack(fminf(fabsf(v0), 128.0f), fminf(fabsf(v1), 128.0f)), scale), t0, t1);
+    f2_unpack(f2_mul(f2_pack(fminf(fabsf(v2), 128.0f), fminf(fabsf(v3), 128.0f)), scale), t2, t3);
+    const float e0 = exp2_fast(t0), e1 = exp2_fast(t1), e2 = exp2_fast(t2), e3 = exp2_fast(t3);
+    const uint64_t da = f2_add(f2_pack(e0, e1), one), db = f2_add(f2_pack(e2, e3), one);
+    f2_unpack(f2_mul(da, db), x0, x1);
+    const float r = reciprocal(x0 * x1);
+    const uint64_t y = f2_pack(r * x1, r * x0);
+    const uint64_t na = f2_pack(v0 < 0.0f ? e0 : 1.0f, v1 < 0.0f ? e1 : 1.0f);
+    const uint64_t nb = f2_pack(v2 < 0.0f ? e2 : 1.0f, v3 < 0.0f ? e3 : 1.0f);
+    const uint64_t sa = f2_mul(f2_mul(y, db), na), sb = f2_mul(f2_mul(y, da), nb);   // the sigmoids
+    f2_unpack(f2_mul(f2_pack(v0, v1), sa), v0, v1);
+    f2_unpack(f2_mul(f2_pack(v2, v3), sb), v2, v3);
 }
 
-// Activates N values.  FAST SiLU takes one reciprocal for four values, since the special-function unit is its
-// bound (1.25 operations there per value instead of 2), and its products in packed pairs: with E = 1 + exp(-v),
-// X = (E0 E2, E1 E3) and r = 1 / (X0 X1), the reciprocals of (E0, E1) are (r X1, r X0) (E2, E3) and those of (E2, E3)
-// the same pair times (E0, E1).  With every value above -21 the product of four stays below 2^124; otherwise
-// (or with a NaN, which must not reach its neighbours) each value goes alone.
+// Activates N values.
 template <int ACT, bool FAST, int N>
 __device__ __forceinline__ void activate_all(float (&v)[N]) {
     if constexpr (ACT == WINO_ACT_SILU && FAST && N % 4 == 0) {
-        // (the check comes after the fast results, so that they do not wait for it)
-        const uint64_t scale = f2_pack(-1.4426950408889634f, -1.4426950408889634f), one = f2_pack(1.0f, 1.0f);
-        float w[N], lo[N / 4];
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint64_t va = f2_pack(v[i], v[i + 1]), vb = f2_pack(v[i + 2], v[i + 3]);
-            float t0, t1, t2, t3, x0, x1;
-            f2_unpack(f2_mul(va, scale), t0, t1);
-            f2_unpack(f2_mul(vb, scale), t2, t3);
-            const uint64_t ea = f2_add(f2_pack(exp2_fast(t0), exp2_fast(t1)), one);
-            const uint64_t eb = f2_add(f2_pack(exp2_fast(t2), exp2_fast(t3)), one);
-            f2_unpack(f2_mul(ea, eb), x0, x1);
-            const float r = reciprocal(x0 * x1);
-            const uint64_t y = f2_pack(r * x1, r * x0);
-            f2_unpack(f2_mul(va, f2_mul(y, eb)), w[i], w[i + 1]);
-            f2_unpack(f2_mul(vb, f2_mul(y, ea)), w[i + 2], w[i + 3]);
-            lo[i / 4] = min3_nan(min3_nan(v[i], v[i + 1], v[i + 2]), v[i + 3], v[i + 3]);
-        }
-#pragma unroll
-        for (int i = 1; i < N / 4; i += 2) lo[0] = min3_nan(lo[0], lo[i], i + 1 < N / 4 ? lo[i + 1] : lo[i]);
-        if (!(lo[0] > -21.0f)) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) w[i] = silu<true>(v[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = w[i];
+        for (int i = 0; i < N; i += 4) silu_quad(v[i], v[i + 1], v[i + 2], v[i + 3]);
         return;
     }
     if constexpr (ACT == WINO_ACT_GELU && FAST && N % 2 == 0) {
@@ -160,7 +147,10 @@ struct MatmulArgs {
     bool out_bf16;
 };
 // The CUDA-core kernel: any type, size, pitch and alignment.
-cudaError_t launch_matmul_simt(const MatmulArgs& a, cudaStream_t st);
+cudaError_t launch_matmul_simt(const MatmulArgs& a, int num_sms, cudaStream_t st);
+
+// For a few rows (at most 65535 blocks of 16): any type, size, pitch and alignment.
+cudaError_t launch_matmul_rows(const MatmulArgs& a, int num_sms, cudaStream_t st);
 
 // The tensor-core kernels take bf16 operands that TMA can read (16-byte aligned bases and pitches).
 bool matmul_tma_operands(const MatmulArgs& a);
@@ -173,6 +163,7 @@ cudaError_t launch_matmul_tc(const MatmulArgs& a, int bn, int num_sms, cudaStrea
 // the last call of the function, which clears it (0: none).
 cudaError_t group_norm_take_error(int* err);
 cudaError_t matmul_simt_take_error(int* err);
+cudaError_t matmul_rows_take_error(int* err);
 cudaError_t matmul_tc_take_error(int* err);
 
 // Last CUDA error of the calling thread's calls without a plan.

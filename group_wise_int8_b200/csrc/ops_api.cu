@@ -34,6 +34,16 @@ int sms() {
     return cached[dev];
 }
 
+// Which kernel: a few rows, the tensor cores where TMA can read the operands, the CUDA cores otherwise.  Against the
+// tensor cores (bf16) the row kernel wins up to 8 rows (8 x 1280 -> 1280: 5.4 us against 6.4; 16 rows: 7.5 against 6.8);
+// against the tiles of the CUDA cores, which need many tiles to be fast, up to about 450000 outputs (fp32, 128 x 1280
+// -> 1280: 30 us against 55; 300 x 640 -> 640: 23 against 29; 512 x 1280 -> 1280: 114 against 97).
+cudaError_t launch_matmul(const MatmulArgs& a, int num_sms, cudaStream_t st) {
+    const bool tma = matmul_tma_operands(a);
+    if (tma ? a.M <= 8 : a.M <= 16 || (double)a.M * a.N <= 450000.0) return launch_matmul_rows(a, num_sms, st);
+    return tma ? launch_matmul_tc(a, 0, num_sms, st) : launch_matmul_simt(a, num_sms, st);
+}
+
 bool natural(const void* p, size_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
 bool dtype_ok(int t) { return t == WINO_F32 || t == WINO_BF16; }
 size_t size_of(int t) { return t == WINO_BF16 ? 2 : 4; }
@@ -164,7 +174,7 @@ int wino_matmul(const wino_matmul_args* g, void* stream) {
     a.out_bf16 = g->out_dtype == WINO_BF16;
     nvtxRangePushA("wino: matmul");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = a.M > 16 && matmul_tma_operands(a) ? launch_matmul_tc(a, 0, sms(), st) : launch_matmul_simt(a, st);
+    const cudaError_t e = launch_matmul(a, sms(), st);
     nvtxRangePop();
     return status(e);
 }
@@ -173,7 +183,7 @@ int wino_check_device_error_ops(void* stream) {
     cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return status(e);
     int first = 0;
-    for (auto take : {group_norm_take_error, matmul_simt_take_error, matmul_tc_take_error}) {
+    for (auto take : {group_norm_take_error, matmul_simt_take_error, matmul_rows_take_error, matmul_tc_take_error}) {
         int v = 0;
         if ((e = take(&v)) != cudaSuccess) return status(e);
         if (first == 0) first = v;

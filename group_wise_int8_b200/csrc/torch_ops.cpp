@@ -10,6 +10,7 @@
 #include <torch/csrc/utils/object_ptr.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -97,6 +98,11 @@ at::ScalarType dtype_or(PyObject* o, at::ScalarType otherwise) {
     return reinterpret_cast<THPDtype*>(o)->scalar_type;
 }
 
+// (at::empty without its dispatch)
+at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor& like) {
+    return at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt);
+}
+
 template <typename F>
 PyObject* guarded(F&& f) {
     try {
@@ -154,7 +160,7 @@ PyObject* group_norm(PyObject*, PyObject* const* o, Py_ssize_t n) {
                 refuse("out must be [N][H][W][C + C2] of out_dtype");
         }
         const c10::cuda::OptionalCUDAGuard guard(x.device());
-        const at::Tensor out = given ? *given : at::empty(shape, x.options().dtype(odtype).requires_grad(false));
+        const at::Tensor out = given ? *given : new_tensor(shape, odtype, x);
         g.x = x.data_ptr();
         g.y = out.data_ptr();
         g.x_pitch = pitch_of("x", x);
@@ -219,7 +225,7 @@ PyObject* matmul(PyObject*, PyObject* const* o, Py_ssize_t n) {
             g.residual_pitch = pitch_of("residual", *residual);
         }
         const c10::cuda::OptionalCUDAGuard guard(a.device());
-        const at::Tensor out = given ? *given : at::empty(shape, a.options().dtype(odtype).requires_grad(false));
+        const at::Tensor out = given ? *given : new_tensor(shape, odtype, a);
         g.a = a.data_ptr();
         g.w = w.data_ptr();
         g.out = out.data_ptr();
