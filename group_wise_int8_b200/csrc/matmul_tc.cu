@@ -100,6 +100,24 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// A ring's current barrier, asked for its phase one turn ahead: the answer is there when the turn comes.
+struct Peek {
+    int st = 0;
+    uint32_t phase;
+    bool ready = false;
+    __device__ __forceinline__ Peek(uint64_t* bars, uint32_t first_phase) : phase(first_phase) { ready = mbar_test(bars, phase); }
+    __device__ __forceinline__ bool wait(uint64_t* bars, volatile int* abort_flag) const {
+        return __all_sync(0xffffffffu, ready) || warp_wait(&bars[st], phase, abort_flag);
+    }
+    __device__ __forceinline__ void next(uint64_t* bars, int stages) {
+        if (++st == stages) {
+            st = 0;
+            phase ^= 1u;
+        }
+        ready = mbar_test(&bars[st], phase);
+    }
+};
+
 // A pair's tiles, in steps of the grid's pairs (no division on the way).
 struct Tile {
     int t, m, n;             // index, row of tiles, column of tiles
@@ -206,20 +224,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
-        int st = 0;
-        uint32_t phase = 0;
+        Peek ring_at(tail->empty, 1u);
         bool ok = true;
         const uint32_t full0 = map_rank(&tail->full[0], 0);
         for (Tile t = first; ok && t.valid(p); t.next(p)) {
             const int m0 = origin_m(t), n0 = t.n * p.BN + (int)half * (p.BN / 2);
             for (int s = 0; s < steps; s += p.kb) {
-                if (!warp_wait(&tail->empty[st], phase ^ 1u, abort_flag)) {
+                if (!ring_at.wait(tail->empty, abort_flag)) {
                     ok = false;
                     break;
                 }
+                const int st = ring_at.st, blocks = min(p.kb, steps - s);
+                ring_at.next(tail->empty, p.stages);
                 const uint32_t bar = full0 + 8u * (uint32_t)st;
                 unsigned char* dst = smem + (size_t)st * stage_bytes;
-                const int blocks = min(p.kb, steps - s);
                 if (elect_one()) {
                     if (half == 0) mbar_arrive_expect_tx(&tail->full[st], 2u * (uint32_t)blocks * block_bytes);
 #pragma unroll
@@ -231,11 +249,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_2d_pair(dst + j * block_bytes + kABytes, second ? &tmW1 : &tmW0, bar, k, n0);
                         }
                 }
-                __syncwarp();
-                if (++st == p.stages) {
-                    st = 0;
-                    phase ^= 1u;
-                }
             }
         }
     } else if (warp == 1) {
@@ -245,9 +258,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const uint64_t a_desc = smem_desc_kmajor(smem_u32(smem), 128);
             const uint64_t w_desc = smem_desc_kmajor(smem_u32(smem) + kABytes, 128);
             const int last0 = (p.m.K0 - (p.steps0 - 1) * kBK + 15) / 16;                 // K-steps of 16 in a source's
-            const int last1 = p.steps1 ? (p.m.K1 - (p.steps1 - 1) * kBK + 15) / 16 : 0;  // last stage
-            int st = 0, it = 0;
-            uint32_t phase = 0;
+            const int last1 = p.steps1 ? (p.m.K1 - (p.steps1 - 1) * kBK + 15) / 16 : 0;  // last block
+            Peek ring_at(tail->full, 0u);
+            int it = 0;
             bool ok = true;
             for (Tile t = first; ok && t.valid(p); t.next(p), ++it) {
                 const int b = it & 1;
@@ -255,13 +268,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)b * 256u;
                 for (int s = 0; s < steps; s += p.kb) {
-                    if (!warp_wait(&tail->full[st], phase, abort_flag)) {
+                    if (!ring_at.wait(tail->full, abort_flag)) {
                         ok = false;
                         break;
                     }
+                    const int st = ring_at.st, blocks = min(p.kb, steps - s);
+                    ring_at.next(tail->full, p.stages);
                     tc_fence_after();
                     const uint32_t off = (uint32_t)st * (stage_bytes >> 4);
-                    const int blocks = min(p.kb, steps - s);
                     if (elect_one()) {
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
@@ -274,11 +288,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             }
                         mma_commit_pair(&tail->empty[st], mask);
                         if (s + p.kb >= steps) mma_commit_pair(&tail->acc_full[b], mask);
-                    }
-                    __syncwarp();
-                    if (++st == p.stages) {
-                        st = 0;
-                        phase ^= 1u;
                     }
                 }
             }
