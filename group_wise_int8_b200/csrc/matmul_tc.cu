@@ -23,7 +23,7 @@
 //               quadrants) that take the tile's 64-column (fp32 output: 32) chunks in turn: fp32
 //               accumulator + bias, activation, + residual, rounded once into a chunk
 //               buffer (64- or 128-byte swizzle) that holds the residual chunk.
-// Outputs or residuals whose base or pitch is no multiple of 16 bytes (an odd
+// Outputs or residuals whose base, pitch or row length is no multiple of 16 bytes (an odd
 // number of columns) cannot go through TMA: there (DIRECT) each warp moves its own
 // 32 rows between the chunk buffer and memory, a row of 32 columns at a time.
 // Every mbarrier wait is bounded; on expiry the CTA records the error and leaves.
@@ -549,7 +549,8 @@ cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStrea
     a.steps0 = (m.K0 + kBK - 1) / kBK;
     a.steps1 = (m.K1 + kBK - 1) / kBK;
     const size_t so = m.out_bf16 ? 2 : 4;
-    const bool direct = !tma_ok(m.out, m.ldo, m.M, so) || (m.res && !tma_ok(m.res, m.ldr, m.M, so));
+    // (a TMA store writes whole 16-byte units: a row that ends inside one would have zeros written behind it)
+    const bool direct = (size_t)m.N * so % 16 != 0 || !tma_ok(m.out, m.ldo, m.M, so) || (m.res && !tma_ok(m.res, m.ldr, m.M, so));
     CUtensorMap map[4], out, res, out_half, res_half;
     if (!matmul_operand_maps(m, a.BN / 2, map)) return cudaErrorInvalidValue;
     out = res = out_half = res_half = map[0];

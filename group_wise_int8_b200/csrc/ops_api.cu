@@ -107,7 +107,7 @@ int wino_group_norm(const wino_group_norm_args* g, void* stream) {
         overlap(region(g->add, (size_t)g->N, (size_t)C, C, 4), y) || overlap(region(g->gamma, 1, (size_t)C, C, 4), y) ||
         overlap(region(g->beta, 1, (size_t)C, C, 4), y))
         return WINO_ERR_INVALID_ARG;
-    if (C > WINO_GROUP_NORM_MAX_CHANNELS) return WINO_ERR_UNSUPPORTED;
+    if (C > WINO_GROUP_NORM_MAX_CHANNELS || g->N > WINO_GROUP_NORM_MAX_IMAGES) return WINO_ERR_UNSUPPORTED;
     GroupNormArgs a = {};
     a.x = g->x;
     a.x2 = g->x2;

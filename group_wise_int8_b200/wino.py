@@ -41,7 +41,8 @@ YGROUPS_TILE, YGROUPS_TAP = 0, 1
 VARIANT_SWAPPED_GEMM, VARIANT_SPLIT_INPUT, VARIANT_SPLIT_OUTPUT, VARIANT_FUSED, VARIANT_A_RESIDENT = 1, 2, 4, 8, 16
 FUSED_AUTO, FUSED_OFF, FUSED_ON = 0, 1, 2
 ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
-GROUP_NORM_MAX_CHANNELS = 16384   # WINO_GROUP_NORM_MAX_CHANNELS
+GROUP_NORM_MAX_CHANNELS = 16384      # WINO_GROUP_NORM_MAX_CHANNELS
+GROUP_NORM_MAX_IMAGES = 1000000000   # WINO_GROUP_NORM_MAX_IMAGES
 DUMP_VQ, DUMP_SV, DUMP_YQ, DUMP_SY, DUMP_Y32, DUMP_ACC32 = range(6)
 NOALLOC_SCRATCH_BYTES = 64 << 20   # WINO_NOALLOC_SCRATCH_BYTES
 
@@ -339,6 +340,8 @@ def load_torch_ops(variant: str = "release"):
 def _on_stream(stream, f, tensors):
     """f() with `stream` current: its output comes from that stream's memory pool, and the tensors' memory is not
     handed out again before the work on that stream is over."""
+    if tensors[0].device != stream.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, tensors[0].device))
     with torch.cuda.stream(stream):
         r = f()
     for t in tensors:

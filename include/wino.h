@@ -355,8 +355,9 @@ int wino_last_cuda_error(wino_plan_t plan);
  * the same NHWC activations.  They need no plan and no workspace, launch one
  * kernel on `stream` and return (asynchronous; capturable in a CUDA graph).  The
  * current device must be the stream's, and every pointer must be of that
- * device.  Results repeat bit for bit.  Pointers need their element type's
- * alignment only; 16-byte aligned bases and pitches (in bytes) run fastest.
+ * device.  The same call repeats bit for bit (the order of the sums goes by the
+ * sizes, the number of images or rows among them).  Pointers need their element
+ * type's alignment only; 16-byte aligned bases and pitches (in bytes) run fastest.
  * A pitch is the distance in elements between consecutive pixels (rows); it is
  * at least the row's length, so a tensor may be a channel range of a wider one.
  * An output may not share memory with an input, but for the in-place forms
@@ -366,6 +367,7 @@ int wino_last_cuda_error(wino_plan_t plan);
 #define WINO_ACT_GELU 2 /* v * Phi(v), Phi the normal distribution function (the erf form) */
 
 #define WINO_GROUP_NORM_MAX_CHANNELS 16384
+#define WINO_GROUP_NORM_MAX_IMAGES 1000000000
 
 /*
  * wino_group_norm -- group normalisation over NHWC pixels, then an activation:
@@ -383,8 +385,9 @@ int wino_last_cuda_error(wino_plan_t plan);
  * Statistics are fp32 sums around a pivot, so a mean that is large against the
  * spread costs no digits; y is rounded once (to nearest even).
  * Errors: INVALID_ARG (sizes not positive, (C + C2) % groups != 0, pitch, type,
- * alignment, overlap, eps negative or not finite), UNSUPPORTED (C + C2 above
- * WINO_GROUP_NORM_MAX_CHANNELS), CUDA.
+ * alignment, overlap, eps negative or not finite; more than 2^30 pixels an image
+ * or 2^40 values), UNSUPPORTED (C + C2 above WINO_GROUP_NORM_MAX_CHANNELS, N above
+ * WINO_GROUP_NORM_MAX_IMAGES), CUDA.
  */
 typedef struct wino_group_norm_args {
     const void* x;
@@ -414,8 +417,11 @@ int wino_group_norm(const wino_group_norm_args* args, void* stream);
  *   out      [M][N], pitch out_pitch, out_dtype.
  * Sums, activation and the residual's addition are fp32 (bf16 products are
  * exact in it); out is rounded once (to nearest even).
- * Errors: INVALID_ARG (sizes not positive, pitch, type, alignment, overlap),
- * CUDA.
+ * bf16 operands whose bases and pitches are multiples of 16 bytes (and K of 8
+ * when there is an a2) run on the tensor cores; others, and fp32 ones, on the
+ * CUDA cores.
+ * Errors: INVALID_ARG (sizes not positive or above 2^31 - 1025, more than 2^40
+ * values in a matrix, pitch, type, alignment, overlap), CUDA.
  */
 typedef struct wino_matmul_args {
     const void* a;

@@ -194,6 +194,20 @@ def test_group_norm_ranges_of_one_buffer_and_in_place(cuda_dev):
         assert torch.equal(y, want)
 
 
+def test_group_norm_beyond_32_bit_offsets(cuda_dev):
+    """2.2e9 values: the first, a middle and the last image against 64 bits.  (Not against a call on that image alone bit
+    for bit: the split, and with it the order of the sums, goes by the number of images too.)"""
+    N, S, C = 33, 256, 1024
+    x = torch.empty(N, S, S, C, device="cuda", dtype=BF16)
+    for n in range(N):
+        x[n].normal_(mean=0.1 * n)
+    y = wino.group_norm(x, 32, act=wino.ACT_SILU)
+    for n in (0, N // 2, N - 1):
+        want, tol = ref_norm(x[n:n + 1], 32, None, None, 1e-5, "silu", None, None, BF16)
+        check(y[n:n + 1], want, tol, "image %d" % n)
+        del want, tol
+
+
 # ---------------------------------------------------------------- matmul
 def ref_matmul(a, w, bias, act, residual, a2, out_dtype):
     A = a.double().reshape(-1, a.shape[-1])
@@ -313,6 +327,32 @@ def test_matmul_non_finite_stays_in_its_row_and_column(cuda_dev, M, K, N, bad):
     w2[N - 1, 0] = bad
     y = wino.matmul(a, w2)
     assert torch.equal(y[:, :N - 1], clean[:, :N - 1]) and not torch.isfinite(y[:, N - 1]).any()
+
+
+@pytest.mark.parametrize("M,K,K2,N,out", [(300, 77, 0, 45, BF16), (300, 77, 0, 45, F32), (140, 40, 27, 333, BF16),
+                                          (9001, 64, 0, 517, BF16), (40, 200, 8, 3, F32), (2000, 129, 0, 65, BF16)])
+def test_matmul_odd_sizes_in_padded_rows(cuda_dev, M, K, K2, N, out):
+    """Sizes that are no multiple of anything in rows padded to 16 bytes: the padding is neither read into a result
+    (it holds NaN) nor written (it holds a mark)."""
+    def padded(seed, rows, cols, dt):
+        t = torch.full((rows, (cols + 7) // 8 * 8 + 8), float("nan"), device="cuda", dtype=dt)
+        t[:, :cols] = randn(seed, rows, cols, dtype=dt)
+        return t[:, :cols]
+    outer = torch.full((M + 3, (N + 7) // 8 * 8 + 8), 7.0, device="cuda", dtype=out)
+    run_matmul(padded(1, M, K, BF16), padded(2, N, K + K2, BF16), randn(3, N), "gelu", padded(4, M, N, out),
+               padded(5, M, K2, BF16) if K2 else None, out=outer[:M, :N])
+    assert (outer[M:] == 7.0).all() and (outer[:, N:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,K,N", [(2200000, 1024, 40), (70000, 64, 32768), (33, 64, 40)])
+def test_matmul_beyond_32_bit_offsets(cuda_dev, M, K, N):
+    """More than 2^31 values in a, or in the output: a row's result does not depend on the rows before it."""
+    a = torch.empty(M, K, device="cuda", dtype=BF16).normal_()
+    w = randn(2, N, K, dtype=BF16)
+    y = wino.matmul(a, w)
+    for lo in (0, M // 2 // 256 * 256, max(0, M - 200) // 256 * 256):
+        part = a[lo:lo + 256].clone()
+        assert torch.equal(y[lo:lo + part.shape[0]], wino.matmul(part, w))
 
 
 def test_matmul_residual_of_infinities(cuda_dev):
@@ -455,6 +495,59 @@ def test_explicit_stream(cuda_dev):
     got = wino.group_norm(x, 8, stream=st), wino.matmul(a, w, stream=st)
     st.synchronize()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+FIRST_CALL_IN_CAPTURE = """
+import torch
+from group_wise_int8_b200 import wino
+x = torch.randn(2, 16, 16, 64, device="cuda", dtype=torch.bfloat16)
+a, w = torch.randn(700, 64, device="cuda", dtype=torch.bfloat16), torch.randn(96, 64, device="cuda", dtype=torch.bfloat16)
+f, v = torch.randn(700, 64, device="cuda"), torch.randn(96, 64, device="cuda")
+wino.load_torch_ops()
+g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):
+    y = wino.group_norm(x, 8, act=wino.ACT_SILU)
+    z = wino.matmul(a, w), wino.matmul(f, v), wino.matmul(a[:2], w)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, wino.group_norm(x, 8, act=wino.ACT_SILU))
+assert torch.equal(z[0], wino.matmul(a, w)) and torch.equal(z[1], wino.matmul(f, v)) and torch.equal(z[2], wino.matmul(a[:2], w))
+print("captured")
+"""
+
+
+def test_first_call_in_a_capture(cuda_dev):
+    """A process whose very first calls are captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
+
+
+def test_two_host_threads(cuda_dev):
+    """Calls from two threads, each on a stream of its own."""
+    import threading
+    states = [_state(700), _state(800)]
+    want = [{n: f(s).clone() for n, f in CALLS.items()} for s in states]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(s, w):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                for n, f in CALLS.items():
+                    if not torch.equal(f(s), w[n]):
+                        failed.append(n)
+            torch.cuda.current_stream().synchronize()
+    threads = [threading.Thread(target=work, args=p) for p in zip(states, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
 
 
 def test_binding_refusals(cuda_dev):

@@ -61,6 +61,7 @@ def test_group_norm_refuses(lib, kw):
 def test_group_norm_refuses_too_many_channels(lib):
     C = wino.GROUP_NORM_MAX_CHANNELS + 32
     assert norm(lib, C=C, x_pitch=C, y_pitch=C) == wino.ERR_UNSUPPORTED
+    assert norm(lib, N=wino.GROUP_NORM_MAX_IMAGES + 1, H=1, W=1, C=32, x_pitch=32, y_pitch=32, x=P[0], y=1 << 50) == wino.ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("kw", [
@@ -125,7 +126,8 @@ def test_packing_matches_the_header(tmp_path, struct, name, fields):
 def test_binding_constants_match_the_header():
     src = open(os.path.join(ROOT, "include", "wino.h")).read()
     for name, value in (("WINO_ACT_NONE", wino.ACT_NONE), ("WINO_ACT_SILU", wino.ACT_SILU), ("WINO_ACT_GELU", wino.ACT_GELU),
-                        ("WINO_GROUP_NORM_MAX_CHANNELS", wino.GROUP_NORM_MAX_CHANNELS)):
+                        ("WINO_GROUP_NORM_MAX_CHANNELS", wino.GROUP_NORM_MAX_CHANNELS),
+                        ("WINO_GROUP_NORM_MAX_IMAGES", wino.GROUP_NORM_MAX_IMAGES)):
         assert "#define %s %d" % (name, value) in src
 
 
