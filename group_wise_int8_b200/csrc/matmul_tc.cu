@@ -566,7 +566,7 @@ cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStrea
     }
     // two K blocks per stage where their MMAs take less time than the issue loops' turn (about 340 cycles; a block
     // takes 2 BN), as long as three stages fit
-    a.kb = a.BN <= 160 ? 2 : 1;
+    a.kb = a.BN <= 128 ? 2 : 1;
     a.stages = kMaxStages;
     while (a.stages > 2 && smem_bytes(a, direct) > kSmemBudget) --a.stages;
     const size_t smem = smem_bytes(a, direct);
