@@ -25,7 +25,8 @@
 //               buffer (64- or 128-byte swizzle) that holds the residual chunk.
 // Outputs or residuals whose base, pitch or row length is no multiple of 16 bytes (an odd
 // number of columns) cannot go through TMA: there (DIRECT) each warp moves its own
-// 32 rows between the chunk buffer and memory, a row of 32 columns at a time.
+// 32 rows between the chunk buffer and memory, a row of 32 columns at a time; a lane's 32 residual values of the
+// next chunk wait in registers (fetched and stored one by one, every load stood behind the store before it).
 // Every mbarrier wait is bounded; on expiry the CTA records the error and leaves.
 #include <algorithm>
 #include <type_traits>
@@ -342,23 +343,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int it = 0, buf = 0;
         uint32_t rphase = 0;
         bool ok = true;
+        // DIRECT: this lane's column of the residual in the warp's 32 rows of the next chunk, on its way before that starts
+        TO res_next[DIRECT ? 32 : 1];
+        auto fetch_res = [&](const Tile& t, int c) {
+            if constexpr (DIRECT) {
+                const TO* res = static_cast<const TO*>(p.m.res);
+                const int n = origin_n(t, c) + lane, m = origin_m(t) + 32 * quad;
+                const bool on = has_res && t.valid(p) && n < p.m.N;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    res_next[i] = TO(0.0f);
+                    if (on && m + i < p.m.M) res_next[i] = res[(size_t)(m + i) * p.m.ldr + n];
+                }
+            }
+        };
         // One chunk of W columns at column n0 of the output, from TMEM column `tcol`; `last`: this warp's last read of
         // accumulator b.
-        auto chunk = [&](auto width, int n0, int m0, uint32_t tcol, int b, bool last) {
+        auto chunk = [&](auto width, int n0, int m0, uint32_t tcol, int b, bool last, auto prefetch) {
             constexpr int W = decltype(width)::value, ROW = W * (int)sizeof(TO), PER = 16 / (int)sizeof(TO);
             unsigned char* cb = ring + (size_t)buf * Ch::kBytes;
             uint32_t r[W];
 #pragma unroll
             for (int j = 0; j < W; j += 32) tmem_ld<32>(t_lane + tcol + (uint32_t)j, *reinterpret_cast<uint32_t(*)[32]>(r + j));
-            if (DIRECT && has_res) {
-                const TO* res = static_cast<const TO*>(p.m.res);
-                const int rows = min(32, p.m.M - m0 - 32 * quad);
-                if (n0 + lane < p.m.N)
-#pragma unroll 8
-                    for (int i = 0; i < rows; ++i)
-                        *reinterpret_cast<TO*>(cb + chunk_unit<ROW>(32 * quad + i, lane / PER) + lane % PER * sizeof(TO)) =
-                            res[(size_t)(m0 + 32 * quad + i) * p.m.ldr + n0 + lane];
-            }
+            if (DIRECT && has_res)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    *reinterpret_cast<TO*>(cb + chunk_unit<ROW>(32 * quad + i, lane / PER) + lane % PER * sizeof(TO)) = res_next[i];
+            prefetch();
             __syncwarp();
             tmem_ld_wait();
             tmem_regs_ready(r);
@@ -447,6 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         };
         fetch_bias(first, g);
+        fetch_res(first, g);
         Tile following = first;
         for (Tile t = first; ok && t.valid(p); t = following, ++it) {
             const int b = it & 1;
@@ -459,12 +471,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < CW / 32; ++j) bias_s[32 * j + lane] = bias_next[j];
                 if (c + 2 < nch) fetch_bias(t, c + 2);
                 else fetch_bias(following, g);
+                auto prefetch = [&]() {
+                    if (c + 2 < nch) fetch_res(t, c + 2);
+                    else fetch_res(following, g);
+                };
                 const uint32_t tcol = (uint32_t)(b * 256 + c * CW);
-                if (half_chunk(c)) chunk(std::integral_constant<int, 32>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch);
-                else chunk(std::integral_constant<int, CW>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch);
+                if (half_chunk(c)) chunk(std::integral_constant<int, 32>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch, prefetch);
+                else chunk(std::integral_constant<int, CW>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch, prefetch);
             }
             if (g >= nch) {   // a tile of one chunk leaves the second group nothing to read
                 fetch_bias(following, g);
+                fetch_res(following, g);
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
             }
