@@ -128,6 +128,8 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// All of them, those in no group yet too.
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_norm_kernel(const GroupNorm
             t[i * entries] = make_float2(p[i] + dm, fmaf(-sum[i], dm, q[i]));
         }
     }
-    copy_wait<0>();   // (a thread without rows has copied parameters)
+    copy_wait_all();   // (a thread without rows, or of the one-value path, has copied parameters outside any group)
     __syncthreads();
 
     // ---- join the row offsets of each channel: `lanes` lanes of a warp per channel
@@ -579,8 +581,8 @@ bool aligned(const void* p, long ld_bytes, size_t to) {
 
 // The split with the least estimated time: rounds of two CTAs per SM, each a fixed part (launch, joins, exchange)
 // plus its share of the input.  The constants are fits to measured splits (in us; 8 x 64 x 64 x 320 bf16 with SiLU takes
-// 16.1 as 256 CTAs of 82 KiB in clusters of 8, 21.3 as 512 of 41 KiB; 8 x 32 x 32 x 640 9.9 in clusters of 4, 22.3
-// in clusters of 16, which leave SMs idle).
+// 16.2 as 256 CTAs of 82 KiB in clusters of 8, 20.5 as 512 of 41 KiB; 8 x 32 x 32 x 640 9.2 in clusters of 4, and
+// clusters of 16 leave SMs idle).
 GroupNormSplit group_norm_split(const GroupNormArgs& a, int vec, int num_sms) {
     const int cg = (a.C0 + a.C1) / a.groups, es = a.x_bf16 ? 2 : 4;
     const int unit = vec / gcd(cg, vec);   // groups of the narrowest slab of whole vectors
