@@ -128,8 +128,6 @@ template <int N>
 __device__ __forceinline__ void copy_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// All of them, those in no group yet too.
-__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
@@ -342,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 2) group_norm_kernel(const GroupNorm
             t[i * entries] = make_float2(p[i] + dm, fmaf(-sum[i], dm, q[i]));
         }
     }
-    copy_wait_all();   // (a thread without rows, or of the one-value path, has copied parameters outside any group)
+    sm100::copy_wait_all();   // (a thread without rows, or of the one-value path, has copied parameters outside any group)
     __syncthreads();
 
     // ---- join the row offsets of each channel: `lanes` lanes of a warp per channel

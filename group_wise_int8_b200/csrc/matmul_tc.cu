@@ -24,9 +24,12 @@
 //               accumulator + bias, activation, + residual, rounded once into a chunk
 //               buffer (64- or 128-byte swizzle) that holds the residual chunk.
 // Outputs or residuals whose base, pitch or row length is no multiple of 16 bytes (an odd
-// number of columns) cannot go through TMA: there (DIRECT) each warp moves its own
-// 32 rows between the chunk buffer and memory, a row of 32 columns at a time; a lane's 32 residual values of the
-// next chunk wait in registers (fetched and stored one by one, every load stood behind the store before it).
+// number of columns) cannot go through TMA: there (DIRECT) each warp moves its own 32 rows, in 16-byte
+// units as they lie in memory.  A row starts anywhere in a unit: the thread that holds the row shifts its
+// packed values by that much (a few selects and byte permutes), the part of a unit that a chunk leaves
+// over goes in front of the next chunk (an epilogue group takes consecutive chunks for that), and only the
+// ends of a group's part of a row are stored value by value.  Residual units come in by
+// asynchronous copies a chunk ahead and are shifted back.
 // Every mbarrier wait is bounded; on expiry the CTA records the error and leaves.
 #include <algorithm>
 #include <type_traits>
@@ -56,17 +59,32 @@ struct TcArgs {
 };
 
 // Epilogue chunks: 128 rows of 128 bytes (64 bf16 or 32 fp32 columns) in the 128-byte swizzle; where a tile's width
-// leaves half a bf16 chunk, and in the DIRECT kernels, 32 columns.
-template <typename TO, bool DIRECT>
-struct Chunk {
-    static constexpr int kCols = DIRECT ? 32 : 128 / (int)sizeof(TO);
-    static constexpr int kBytes = kARows * kCols * (int)sizeof(TO);
-    static constexpr int kBuffers = DIRECT ? 1 : 2;   // per epilogue group
-};
+// leaves half a bf16 chunk, 32 columns.
+constexpr int kChunkBytes = kARows * 128;
+constexpr int kBuffers = 2;   // per epilogue group
+// DIRECT: a warp's 32 rows of a chunk's units and the one that it shares with its neighbour; 144 bytes apart, so that neither a
+// row's owner nor the copies between a row and memory meet bank conflicts.
+constexpr int kRowPitch = 128 + 16;
+constexpr int kRowsBytes = 32 * kRowPitch;
 // Byte offset of 16-byte unit j of a row of ROW bytes (64 or 128: the TMA swizzle of that width).
 template <int ROW>
 __device__ __forceinline__ uint32_t chunk_unit(int row, int j) {
     return (uint32_t)(row * ROW + ((j ^ (ROW == 64 ? (row >> 1) & 3 : row & 7)) << 4));
+}
+
+// p[j] = the word `elems` values of SIZE bytes (fewer than 16 bytes) behind word j, in place.
+template <int SIZE, int N>
+__device__ __forceinline__ void shift_words(uint32_t (&p)[N], int elems) {
+    const int f = elems * SIZE / 4;
+#pragma unroll
+    for (int j = 0; j + 2 < N; ++j) p[j] = f & 2 ? p[j + 2] : p[j];
+#pragma unroll
+    for (int j = 0; j + 1 < N; ++j) p[j] = f & 1 ? p[j + 1] : p[j];
+    if constexpr (SIZE == 2) {
+        const uint32_t sel = elems & 1 ? 0x5432u : 0x3210u;
+#pragma unroll
+        for (int j = 0; j < N; ++j) p[j] = __byte_perm(p[j], j + 1 < N ? p[j + 1] : 0u, sel);
+    }
 }
 
 struct Tail {
@@ -168,6 +186,11 @@ struct Cursor {
     }
 };
 
+// All chunk buffers of a CTA.
+__host__ __device__ constexpr int chunk_bytes(bool direct, bool res) {
+    return direct ? (res ? 2 : 1) * 8 * kRowsBytes : 2 * kBuffers * kChunkBytes;
+}
+
 template <typename TO, bool DIRECT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     matmul_tc_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
@@ -175,14 +198,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes,
                      const __grid_constant__ CUtensorMap tmOutHalf, const __grid_constant__ CUtensorMap tmResHalf,
                      const TcArgs p) {
-    using Ch = Chunk<TO, DIRECT>;
-    constexpr int NB = Ch::kBuffers, CW = Ch::kCols;
+    constexpr int NB = kBuffers, CW = 128 / (int)sizeof(TO);
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t block_bytes = kABytes + (uint32_t)(p.BN / 2) * kBK * 2;   // one K block of A, then of W
     const uint32_t stage_bytes = (uint32_t)p.kb * block_bytes;
-    unsigned char* chunks = smem + (size_t)p.stages * stage_bytes;   // [2 groups][NB][Ch::kBytes]
-    Tail* tail = reinterpret_cast<Tail*>(chunks + 2 * NB * Ch::kBytes);
+    // [2 groups][NB][kChunkBytes], or [output, residual if any][8 warps][kRowsBytes]
+    unsigned char* chunks = smem + (size_t)p.stages * stage_bytes;
+    Tail* tail = reinterpret_cast<Tail*>(chunks + chunk_bytes(DIRECT, p.m.res != nullptr));
     volatile int* abort_flag = &tail->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t half = cluster_rank() & 1u;   // 0: the pair's leader, rows 0..127 of its tiles
@@ -297,15 +320,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // -------------------------------------- chunk buffers of one epilogue group
         if constexpr (!DIRECT) {
             const int g = warp - 2;
-            unsigned char* ring = chunks + (size_t)g * NB * Ch::kBytes;
+            unsigned char* ring = chunks + (size_t)g * NB * kChunkBytes;
             Cursor<CW> cur(first, g, p), ahead = cur;
             auto hand_out = [&](int buf) {   // a free buffer, for the chunk at `ahead`
                 if (!has_res) {
                     mbar_arrive(&tail->buf_full[g][buf]);
                 } else if (ahead.valid(p)) {
                     const bool hc = half_chunk(ahead.c);
-                    mbar_arrive_expect_tx(&tail->buf_full[g][buf], hc ? Ch::kBytes / 2 : Ch::kBytes);
-                    tma_load_2d(ring + buf * Ch::kBytes, hc ? &tmResHalf : &tmRes, &tail->buf_full[g][buf],
+                    mbar_arrive_expect_tx(&tail->buf_full[g][buf], hc ? kChunkBytes / 2 : kChunkBytes);
+                    tma_load_2d(ring + buf * kChunkBytes, hc ? &tmResHalf : &tmRes, &tail->buf_full[g][buf],
                                 origin_n(ahead.tile, ahead.c), origin_m(ahead.tile));
                     ahead.next(p);
                 }
@@ -320,7 +343,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     const int m0 = origin_m(cur.tile);
                     if (m0 < p.m.M)
-                        tma_store_2d(half_chunk(cur.c) ? &tmOutHalf : &tmOut, ring + buf * Ch::kBytes, origin_n(cur.tile, cur.c), m0);
+                        tma_store_2d(half_chunk(cur.c) ? &tmOutHalf : &tmOut, ring + buf * kChunkBytes, origin_n(cur.tile, cur.c), m0);
                     bulk_commit();
                     bulk_wait_read<1>();   // the store before this one has read its buffer, which is handed out again
                     if (i > 0) hand_out((buf + NB - 1) % NB);
@@ -337,39 +360,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ----------------------------------------------------------- epilogue
         const int g = (warp - 4) >> 2, quad = warp & 3, row = 32 * quad + lane;
         const uint32_t t_lane = tmem_base + ((uint32_t)(32 * quad) << 16);
-        unsigned char* ring = chunks + (size_t)g * NB * Ch::kBytes;
+        unsigned char* ring = chunks + (size_t)g * NB * kChunkBytes;
         float* bias_s = tail->bias[warp - 4];
         const uint32_t release = map_rank(&tail->acc_empty[0], 0);
         int it = 0, buf = 0;
         uint32_t rphase = 0;
         bool ok = true;
-        // DIRECT: this lane's column of the residual in the warp's 32 rows of the next chunk, on its way before that starts
-        TO res_next[DIRECT ? 32 : 1];
+        // DIRECT: the values of a unit; this warp's rows of the output and of the residual
+        constexpr int E = 16 / (int)sizeof(TO);
+        unsigned char* out_rows = chunks + (size_t)(warp - 4) * kRowsBytes;
+        unsigned char* res_rows = out_rows + 8 * kRowsBytes;
+        uint32_t carry[4] = {0u, 0u, 0u, 0u};   // this row's last unit of the chunk before
+        // a group's chunks of a tile: every other one, or half of them
+        auto first_chunk = [&](const Tile& t) { return DIRECT ? (g ? (chunks_of<CW>(p, t) + 1) / 2 : 0) : g; };
+        auto end_chunk = [&](const Tile& t) { return DIRECT && g == 0 ? (chunks_of<CW>(p, t) + 1) / 2 : chunks_of<CW>(p, t); };
+        constexpr int kChunkStep = DIRECT ? 1 : 2;
+        // DIRECT: the units that hold the residual's chunk c of the warp's rows
         auto fetch_res = [&](const Tile& t, int c) {
             if constexpr (DIRECT) {
-                const TO* res = static_cast<const TO*>(p.m.res);
-                const int n = origin_n(t, c) + lane, m = origin_m(t) + 32 * quad;
-                const bool on = has_res && t.valid(p) && n < p.m.N;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    res_next[i] = TO(0.0f);
-                    if (on && m + i < p.m.M) res_next[i] = res[(size_t)(m + i) * p.m.ldr + n];
+                if (has_res && t.valid(p) && c < end_chunk(t)) {
+                    const TO* res = static_cast<const TO*>(p.m.res);
+                    const int n0 = origin_n(t, c), left = p.m.N - n0, rows = p.m.M - origin_m(t) - 32 * quad, u = lane & 7;
+                    const TO* at = res + (size_t)(p.m.M - rows + (lane >> 3)) * p.m.ldr + n0;
+                    unsigned char* dst = res_rows + (lane >> 3) * kRowPitch + 16 * u;
+#pragma unroll 2
+                    for (int r = lane >> 3; r < min(32, rows); r += 4, at += 4 * p.m.ldr, dst += 4 * kRowPitch) {
+                        const int d = E * u - ((int)(reinterpret_cast<uintptr_t>(at) / sizeof(TO)) & (E - 1));
+                        if (d < left) {
+                            if (at + d >= res) {   // (zeros behind the row's end)
+                                copy_async16(dst, at + d, min(16, (left - d) * (int)sizeof(TO)));
+                            } else {               // the tensor starts inside the unit
+                                for (int e = (int)(res - at) - d; e < E && d + e < left; ++e) reinterpret_cast<TO*>(dst)[e] = at[d + e];
+                            }
+                        }
+                        if (u == 0 && d < 0 && d + 8 * E < left)
+                            copy_async16(dst + 128, at + d + 8 * E, min(16, (left - d - 8 * E) * (int)sizeof(TO)));
+                    }
                 }
             }
         };
         // One chunk of W columns at column n0 of the output, from TMEM column `tcol`; `last`: this warp's last read of
-        // accumulator b.
-        auto chunk = [&](auto width, int n0, int m0, uint32_t tcol, int b, bool last, auto prefetch) {
-            constexpr int W = decltype(width)::value, ROW = W * (int)sizeof(TO), PER = 16 / (int)sizeof(TO);
-            unsigned char* cb = ring + (size_t)buf * Ch::kBytes;
+        // accumulator b; the group's part of the tile's columns: lo to hi.
+        auto chunk = [&](auto width, int n0, int m0, uint32_t tcol, int b, bool last, int lo, int hi, auto prefetch) {
+            constexpr int W = decltype(width)::value, ROW = W * (int)sizeof(TO), UP = ROW / 16;
+            unsigned char* cb = ring + (size_t)buf * kChunkBytes;
             uint32_t r[W];
 #pragma unroll
             for (int j = 0; j < W; j += 32) tmem_ld<32>(t_lane + tcol + (uint32_t)j, *reinterpret_cast<uint32_t(*)[32]>(r + j));
-            if (DIRECT && has_res)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    *reinterpret_cast<TO*>(cb + chunk_unit<ROW>(32 * quad + i, lane / PER) + lane % PER * sizeof(TO)) = res_next[i];
-            prefetch();
             __syncwarp();
             tmem_ld_wait();
             tmem_regs_ready(r);
@@ -393,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 ok = false;
                 return;
             }
-            if (has_res) {
+            if (!DIRECT && has_res) {
 #pragma unroll
                 for (int j = 0; j < ROW / 16; ++j) {
                     const uint4 w = *reinterpret_cast<const uint4*>(cb + chunk_unit<ROW>(row, j));
@@ -408,6 +445,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+            }
+            if constexpr (DIRECT) {
+                const int m = m0 + row;
+                if (has_res) {
+                    copy_wait_all();
+                    __syncwarp();
+                    uint32_t x[4 + ROW / 4];
+#pragma unroll
+                    for (int j = 0; j <= UP; ++j)
+                        *reinterpret_cast<uint4*>(x + 4 * j) = *reinterpret_cast<const uint4*>(res_rows + lane * kRowPitch + 16 * j);
+                    const TO* at = static_cast<const TO*>(p.m.res) + (size_t)m * p.m.ldr + n0;
+                    shift_words<sizeof(TO)>(x, (int)(reinterpret_cast<uintptr_t>(at) / sizeof(TO)) & (E - 1));
+#pragma unroll
+                    for (int j = 0; j < ROW / 4; ++j) {
+                        if constexpr (sizeof(TO) == 2) {
+                            v[2 * j] += __uint_as_float(x[j] << 16);
+                            v[2 * j + 1] += __uint_as_float(x[j] & 0xffff0000u);
+                        } else {
+                            v[j] += __uint_as_float(x[j]);
+                        }
+                    }
+                    __syncwarp();
+                    prefetch();
+                }
+                // unit j of the row in memory: `t` values behind unit j - 1 of the chunk
+                TO* out = static_cast<TO*>(p.m.out);
+                auto ahead = [&](const TO* at) { return (0 - (int)(reinterpret_cast<uintptr_t>(at) / sizeof(TO))) & (E - 1); };
+                uint32_t x[4 + ROW / 4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = carry[j];
+#pragma unroll
+                for (int j = 0; j < ROW / 4; ++j) {
+                    if constexpr (sizeof(TO) == 2) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                        x[4 + j] = *reinterpret_cast<const uint32_t*>(&h);
+                    } else {
+                        x[4 + j] = __float_as_uint(v[j]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) carry[j] = x[ROW / 4 + j];
+                shift_words<sizeof(TO)>(x, ahead(out + (size_t)m * p.m.ldo + n0));
+#pragma unroll
+                for (int j = 0; j <= UP; ++j)
+                    *reinterpret_cast<uint4*>(out_rows + lane * kRowPitch + 16 * j) =
+                        make_uint4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                __syncwarp();
+                // four rows at a time: whole units, and value by value the ends of the group's part of a row
+                const int rows = min(32, p.m.M - m0 - 32 * quad), u = lane & 7, from = lo - n0, to = hi - n0;
+                const unsigned char* src = out_rows + (lane >> 3) * kRowPitch;
+                TO* at = out + (size_t)(m0 + 32 * quad + (lane >> 3)) * p.m.ldo + n0;
+                const TO* end = out + (size_t)(p.m.M - 1) * p.m.ldo + p.m.N;   // (of the debug build's check)
+#pragma unroll 2
+                for (int r = lane >> 3; r < rows; r += 4, at += 4 * p.m.ldo, src += 4 * kRowPitch) {
+                    const int d0 = ahead(at) - E, d = d0 + E * u;   // columns from n0 of the row's first unit and of unit u
+                    if (u < UP && d >= from && d + E <= to && in_bounds((size_t)(at + d + E - 1 - out), (size_t)(end - out), &g_err))
+                        *reinterpret_cast<uint4*>(at + d) = *reinterpret_cast<const uint4*>(src + 16 * u);
+                    auto value = [&](int unit) {
+                        const int x = d0 + E * unit + u;
+                        if (u < E && x >= from && x < to && in_bounds((size_t)(at + x - out), (size_t)(end - out), &g_err))
+                            at[x] = reinterpret_cast<const TO*>(src + 16 * unit)[u];
+                    };
+                    if (from == 0) value(0);
+                    if (W >= to) value(min((to - d0) / E, UP));
+                }
+                __syncwarp();
+                return;
             }
 #pragma unroll
             for (int j = 0; j < ROW / 16; ++j) {
@@ -426,26 +530,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 *reinterpret_cast<uint4*>(cb + chunk_unit<ROW>(row, j)) = w;
             }
-            if constexpr (DIRECT) {
-                __syncwarp();
-                TO* out = static_cast<TO*>(p.m.out);
-                const int rows = min(32, p.m.M - m0 - 32 * quad);
-                const size_t limit = (size_t)(p.m.M - 1) * p.m.ldo + p.m.N;
-                if (n0 + lane < p.m.N)
-#pragma unroll 8
-                    for (int i = 0; i < rows; ++i) {
-                        const size_t at = (size_t)(m0 + 32 * quad + i) * p.m.ldo + n0 + lane;
-                        if (in_bounds(at, limit, &g_err))
-                            out[at] = *reinterpret_cast<const TO*>(cb + chunk_unit<ROW>(32 * quad + i, lane / PER) + lane % PER * sizeof(TO));
-                    }
-            } else {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tail->buf_ready[g][buf]);
-                if (++buf == NB) {
-                    buf = 0;
-                    rphase ^= 1u;
-                }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tail->buf_ready[g][buf]);
+            if (++buf == NB) {
+                buf = 0;
+                rphase ^= 1u;
             }
             __syncwarp();
         };
@@ -457,35 +547,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 bias_next[j] = p.m.bias && n < p.m.N ? p.m.bias[n] : 0.0f;
             }
         };
-        fetch_bias(first, g);
-        fetch_res(first, g);
+        fetch_bias(first, first_chunk(first));
+        fetch_res(first, first_chunk(first));
         Tile following = first;
         for (Tile t = first; ok && t.valid(p); t = following, ++it) {
             const int b = it & 1;
-            const int nch = chunks_of<CW>(p, t), m0 = origin_m(t);
+            const int c0 = first_chunk(t), end = end_chunk(t), m0 = origin_m(t);
+            const int lo = origin_n(t, c0), hi = min(min(origin_n(t, end), origin_n(t, 0) + p.BN), p.m.N);
             following.next(p);
             if (!warp_wait(&tail->acc_full[b], (uint32_t)((it >> 1) & 1), abort_flag)) break;
             tc_fence_after();
-            for (int c = g; ok && c < nch; c += 2) {
+            for (int c = c0; ok && c < end; c += kChunkStep) {
+                const bool last = c + kChunkStep >= end;
 #pragma unroll
                 for (int j = 0; j < CW / 32; ++j) bias_s[32 * j + lane] = bias_next[j];
-                if (c + 2 < nch) fetch_bias(t, c + 2);
-                else fetch_bias(following, g);
+                if (!last) fetch_bias(t, c + kChunkStep);
+                else fetch_bias(following, first_chunk(following));
                 auto prefetch = [&]() {
-                    if (c + 2 < nch) fetch_res(t, c + 2);
-                    else fetch_res(following, g);
+                    if (!last) fetch_res(t, c + kChunkStep);
+                    else fetch_res(following, first_chunk(following));
                 };
                 const uint32_t tcol = (uint32_t)(b * 256 + c * CW);
-                if (half_chunk(c)) chunk(std::integral_constant<int, 32>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch, prefetch);
-                else chunk(std::integral_constant<int, CW>(), origin_n(t, c), m0, tcol, b, c + 2 >= nch, prefetch);
+                if (half_chunk(c)) chunk(std::integral_constant<int, 32>(), origin_n(t, c), m0, tcol, b, last, lo, hi, prefetch);
+                else chunk(std::integral_constant<int, CW>(), origin_n(t, c), m0, tcol, b, last, lo, hi, prefetch);
             }
-            if (g >= nch) {   // a tile of one chunk leaves the second group nothing to read
-                fetch_bias(following, g);
-                fetch_res(following, g);
+            if (c0 >= end) {   // a tile of one chunk leaves the second group nothing to read
+                fetch_bias(following, first_chunk(following));
+                fetch_res(following, first_chunk(following));
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(release + 8u * (uint32_t)b);
             }
         }
+        if (DIRECT) copy_wait_all();
     }
 
     // Every role is done: the MMAs that read either CTA's shared memory have completed (both epilogues waited
@@ -500,9 +593,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 size_t smem_bytes(const TcArgs& a, bool direct) {
-    const size_t chunks = direct ? (a.m.out_bf16 ? Chunk<__nv_bfloat16, true>::kBytes : Chunk<float, true>::kBytes)
-                                 : (size_t)Chunk<float, false>::kBuffers * Chunk<float, false>::kBytes;   // (either type)
-    return 1024 + (size_t)a.stages * a.kb * (kABytes + a.BN / 2 * kBK * 2) + 2 * chunks + sizeof(Tail);
+    return 1024 + (size_t)a.stages * a.kb * (kABytes + a.BN / 2 * kBK * 2) + chunk_bytes(direct, a.m.res != nullptr) + sizeof(Tail);
 }
 
 bool tma_ok(const void* p, long pitch, int rows, size_t es) {

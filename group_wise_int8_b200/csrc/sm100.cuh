@@ -147,6 +147,13 @@ __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
+// 16 bytes global -> shared without a register: the first `bytes` from memory, then zeros.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(bytes) : "memory");
+}
+// Every cp.async of this thread has landed, those in no group yet too.
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // True in one lane of a converged warp.  Loops that issue tensor-core or TMA instructions run in the whole warp, with
 // only the instruction itself under this predicate: their descriptors, coordinates and addresses are then the same in
 // all lanes and stay in uniform registers (inside `if (lane == 0)` each instruction first moves them there).
