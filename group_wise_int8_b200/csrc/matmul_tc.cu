@@ -18,7 +18,7 @@
 //   warp 1    = TMEM allocator; in the leader the MMA issuer; two accumulators of BN columns,
 //               so that the next tile's MMAs run under this tile's epilogue.
 //   warps 2, 3 = the chunk buffers of one epilogue group each: residual chunks in
-//               (TMA, up to four ahead), finished chunks out (TMA store).
+//               (TMA, two to four buffers a group), finished chunks out (TMA store).
 //   warps 4-11 = epilogue, two groups of four warps (the four TMEM lane
 //               quadrants) that take the tile's 64-column (fp32 output: 32) chunks in turn: fp32
 //               accumulator + bias, activation, + residual, rounded once into a chunk
@@ -55,13 +55,13 @@ constexpr size_t kSmemBudget = 226 * 1024;
 
 struct TcArgs {
     MatmulArgs m;
-    int BN, kb, stages, tiles_m, tiles_n, steps0, steps1;   // kb: K blocks of 64 per stage (1 or 2)
+    int BN, kb, stages, buffers, tiles_m, tiles_n, steps0, steps1;   // kb: K blocks of 64 per stage (1 or 2)
 };
 
 // Epilogue chunks: 128 rows of 128 bytes (64 bf16 or 32 fp32 columns) in the 128-byte swizzle; where a tile's width
 // leaves half a bf16 chunk, 32 columns.
 constexpr int kChunkBytes = kARows * 128;
-constexpr int kBuffers = 2;   // per epilogue group
+constexpr int kMaxBuffers = 4;   // per epilogue group
 // DIRECT: a warp's 32 rows of a chunk's units and the one that it shares with its neighbour; 144 bytes apart, so that neither a
 // row's owner nor the copies between a row and memory meet bank conflicts.
 constexpr int kRowPitch = 128 + 16;
@@ -92,8 +92,8 @@ struct Tail {
     uint64_t empty[kMaxStages];    // the pair's MMAs have read the stage
     uint64_t acc_full[2];
     uint64_t acc_empty[2];         // leader: both CTAs' epilogues have read the accumulator
-    uint64_t buf_full[2][2];       // a group's chunk buffer is free to use, its residual (if any) landed
-    uint64_t buf_ready[2][2];      // ... and holds the output chunk: the group's four warps have written it
+    uint64_t buf_full[2][kMaxBuffers];       // a group's chunk buffer is free to use, its residual (if any) landed
+    uint64_t buf_ready[2][kMaxBuffers];      // ... and holds the output chunk: the group's four warps have written it
     alignas(16) float bias[8][64];   // per epilogue warp
     uint32_t tmem_base;
     int abort_flag;
@@ -187,8 +187,8 @@ struct Cursor {
 };
 
 // All chunk buffers of a CTA.
-__host__ __device__ constexpr int chunk_bytes(bool direct, bool res) {
-    return direct ? (res ? 2 : 1) * 8 * kRowsBytes : 2 * kBuffers * kChunkBytes;
+__host__ __device__ constexpr int chunk_bytes(bool direct, bool res, int buffers) {
+    return direct ? (res ? 2 : 1) * 8 * kRowsBytes : 2 * buffers * kChunkBytes;
 }
 
 template <typename TO, bool DIRECT>
@@ -198,14 +198,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes,
                      const __grid_constant__ CUtensorMap tmOutHalf, const __grid_constant__ CUtensorMap tmResHalf,
                      const TcArgs p) {
-    constexpr int NB = kBuffers, CW = 128 / (int)sizeof(TO);
+    constexpr int CW = 128 / (int)sizeof(TO);
+    const int NB = p.buffers;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t block_bytes = kABytes + (uint32_t)(p.BN / 2) * kBK * 2;   // one K block of A, then of W
     const uint32_t stage_bytes = (uint32_t)p.kb * block_bytes;
     // [2 groups][NB][kChunkBytes], or [output, residual if any][8 warps][kRowsBytes]
     unsigned char* chunks = smem + (size_t)p.stages * stage_bytes;
-    Tail* tail = reinterpret_cast<Tail*>(chunks + chunk_bytes(DIRECT, p.m.res != nullptr));
+    Tail* tail = reinterpret_cast<Tail*>(chunks + chunk_bytes(DIRECT, p.m.res != nullptr, p.buffers));
     volatile int* abort_flag = &tail->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t half = cluster_rank() & 1u;   // 0: the pair's leader, rows 0..127 of its tiles
@@ -346,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                         tma_store_2d(half_chunk(cur.c) ? &tmOutHalf : &tmOut, ring + buf * kChunkBytes, origin_n(cur.tile, cur.c), m0);
                     bulk_commit();
                     bulk_wait_read<1>();   // the store before this one has read its buffer, which is handed out again
-                    if (i > 0) hand_out((buf + NB - 1) % NB);
+                    if (i > 0) hand_out(buf ? buf - 1 : NB - 1);
                 }
                 __syncwarp();
                 if (++buf == NB) {
@@ -593,7 +594,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 size_t smem_bytes(const TcArgs& a, bool direct) {
-    return 1024 + (size_t)a.stages * a.kb * (kABytes + a.BN / 2 * kBK * 2) + chunk_bytes(direct, a.m.res != nullptr) + sizeof(Tail);
+    return 1024 + (size_t)a.stages * a.kb * (kABytes + a.BN / 2 * kBK * 2) + chunk_bytes(direct, a.m.res != nullptr, a.buffers) + sizeof(Tail);
 }
 
 bool tma_ok(const void* p, long pitch, int rows, size_t es) {
@@ -675,6 +676,13 @@ cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStrea
     // two K blocks per stage where their MMAs take less time than the issue loops' turn (about 340 cycles; a block
     // takes 2 BN), as long as three stages fit
     a.kb = a.BN <= 128 ? 2 : 1;
+    // Residual chunks wait in the buffers, so that tiles of few K blocks, whose time is the residual's way in, want more of
+    // them, and others more stages (32768 x 320 -> 1280 with residual: 52 us with two buffers, 41 with three; 14778 x 128
+    // -> 2624: 51, 35 and 31 with four; 32768 x 512 -> 640: 30 with two, 33 with three; without a residual two do)
+    const int steps = a.steps0 + a.steps1;
+    a.buffers = !m.res || steps > 6 ? 2 : (steps > 2 ? 3 : kMaxBuffers);
+    a.stages = 2;
+    while (a.buffers > 2 && smem_bytes(a, direct) > kSmemBudget) --a.buffers;
     a.stages = kMaxStages;
     while (a.stages > 2 && smem_bytes(a, direct) > kSmemBudget) --a.stages;
     const size_t smem = smem_bytes(a, direct);
