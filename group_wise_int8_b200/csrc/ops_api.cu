@@ -35,7 +35,7 @@ int sms() {
 }
 
 // Which kernel: a few rows, the tensor cores where TMA can read the operands, the CUDA cores otherwise.  Against the
-// tensor cores (bf16) the row kernel wins up to 8 rows (8 x 1280 -> 1280: 5.4 us against 6.4; 16 rows: 7.5 against 6.8);
+// tensor cores (bf16) the row kernel wins up to 8 rows (8 x 1280 -> 1280: 5.4 us against 6.7; 16 rows: 7.5 against 6.7);
 // against the tiles of the CUDA cores, which need many tiles to be fast, up to about 450000 outputs (fp32, 128 x 1280
 // -> 1280: 30 us against 55; 300 x 640 -> 640: 23 against 29; 512 x 1280 -> 1280: 114 against 97).
 cudaError_t launch_matmul(const MatmulArgs& a, int num_sms, cudaStream_t st) {
