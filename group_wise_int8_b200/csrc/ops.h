@@ -16,7 +16,7 @@ namespace wino {
 // ------------------------------------------------------------ activations
 // SiLU v / (1 + exp(-v)) and GELU v Phi(v) in fp32.  FAST: the result is rounded to bf16 next, so the hardware's
 // exponential and reciprocal (relative error below 2^-20, bf16 rounds at 2^-9) serve; otherwise the
-// accurate expf and an IEEE division.
+// accurate expf (2 ulp) and a reciprocal to 1 ulp: below 2^-21 in all.
 __device__ __forceinline__ float exp2_fast(float v) {   // results below 2^-126 become 0
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
@@ -28,11 +28,17 @@ __device__ __forceinline__ float reciprocal(float v) {
     return r;
 }
 
+__device__ __forceinline__ float reciprocal_full(float v) {   // to 1 ulp, subnormal results too
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 template <bool FAST>
 __device__ __forceinline__ float silu(float v) {
     // exp(-v) = inf (v below about -88) gives v * (1 / inf) = -0
     if (FAST) return reciprocal(1.0f + exp2_fast(v * -1.4426950408889634f)) * v;
-    return v / (1.0f + expf(-v));
+    return v * reciprocal_full(1.0f + expf(-v));
 }
 
 // FAST GELU.  The tail q(a) = Phi(-a) = erfc(a / sqrt 2) / 2, a = |v|, is exp(-a^2 / 2) t P(t) with t = 1 / (1 + 0.3 a)
