@@ -117,6 +117,8 @@ PyObject* guarded(F&& f) {
 
 template <typename Args>
 PyObject* run(Status fn, const Args& args, const at::Tensor& out, PyObject* given) {
+    // (a graph that saved the given tensor for its backward pass finds out, as after torch's own in-place calls)
+    if (given != Py_None) out.unsafeGetTensorImpl()->bump_version();
     const int rc = fn(&args, c10::cuda::getCurrentCUDAStream(out.get_device()).stream());
     if (rc != WINO_OK) return PyLong_FromLong(rc);
     if (given != Py_None) {

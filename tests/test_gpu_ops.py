@@ -314,6 +314,46 @@ def test_matmul_adds_in_place(cuda_dev, M, K, N):
     assert y is res and torch.equal(y, want)
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("out_lo,out_pad,res_lo,res_pad", [(1, 0, 0, 0), (0, 1, 5, 2), (7, 6, 2, 9), (4, 4, 1, 6), (0, 0, 3, 0)])
+@pytest.mark.parametrize("M,N", [(17, 1), (33, 7), (129, 66), (300, 250), (65, 515)])
+def test_matmul_rows_start_anywhere(cuda_dev, out, out_lo, out_pad, res_lo, res_pad, M, N):
+    """Rows of the output and of the residual start at any offset within 16 bytes, each its own; beside them lie NaN
+    (the residual, never read into a result) and marks (the output, never written)."""
+    K = 96
+    wide = torch.full((M, res_lo + N + res_pad), float("nan"), device="cuda", dtype=out)
+    res = wide[:, res_lo:res_lo + N]
+    res.copy_(randn(4, M, N, dtype=out))
+    outer = torch.full((M + 1, out_lo + N + out_pad), 7.0, device="cuda", dtype=out)
+    y = outer[:M, out_lo:out_lo + N]
+    for variant in ("release", "debug"):
+        run_matmul(randn(1, M, K, dtype=BF16), randn(2, N, K, dtype=BF16, spread=K ** -0.5), randn(3, N), "gelu", res, out=y,
+                   variant=variant)
+    rest = torch.ones_like(outer, dtype=torch.bool)
+    rest[:M, out_lo:out_lo + N] = False
+    assert (outer[rest] == 7.0).all() and wino.check_device_error_ops(variant="debug") == wino.OK
+
+
+@pytest.mark.parametrize("M,K,N", [(9001, 64, 517), (9000, 320, 640), (9000, 192, 1280), (20001, 128, 333)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_matmul_many_tiles_of_few_blocks(cuda_dev, M, K, N, in_place):
+    a, w, res = randn(1, M, K, dtype=BF16), randn(2, N, K, dtype=BF16, spread=K ** -0.5), randn(3, M, N, dtype=BF16)
+    run_matmul(a, w, None, "silu", res, **({"out": res} if in_place else {}))
+
+
+def test_given_outputs_count_as_changed(cuda_dev):
+    """A backward pass that saved a tensor which a call then writes raises, as after any in-place change."""
+    x = randn(1, 2, 4, 4, 32).requires_grad_()
+    w, g = randn(2, 32, 32), randn(3, 2, 4, 4, 32)
+    for call in (lambda t: wino.group_norm(g, 4, out=t), lambda t: wino.matmul(g, w, out=t)):
+        h = x * 2.0
+        z = (h * h).sum()
+        with torch.no_grad():
+            call(h)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            z.backward()
+
+
 @pytest.mark.parametrize("M,K,N", [(5, 200, 64), (200, 200, 96), (9000, 128, 640), (512, 2560, 320)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_matmul_non_finite_stays_in_its_row_and_column(cuda_dev, M, K, N, bad):
