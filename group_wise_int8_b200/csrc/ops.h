@@ -156,6 +156,7 @@ struct MatmulArgs {
 cudaError_t launch_matmul_simt(const MatmulArgs& a, int num_sms, cudaStream_t st);
 
 // For a few rows (at most 65535 blocks of 16): any type, size, pitch and alignment.
+constexpr int kMaxRowsM = 8 * 65535;   // rows that the row kernel's grid holds
 cudaError_t launch_matmul_rows(const MatmulArgs& a, int num_sms, cudaStream_t st);
 
 // The tensor-core kernels take bf16 operands that TMA can read (16-byte aligned bases and pitches).

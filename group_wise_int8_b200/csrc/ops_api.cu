@@ -34,13 +34,18 @@ int sms() {
     return cached[dev];
 }
 
-// Which kernel: a few rows, the tensor cores where TMA can read the operands, the CUDA cores otherwise.  Against the
-// tensor cores (bf16) the row kernel wins up to 8 rows (8 x 1280 -> 1280: 5.4 us against 6.7; 16 rows: 7.5 against 6.7);
-// against the tiles of the CUDA cores, which need many tiles to be fast, up to about 450000 outputs (fp32, 128 x 1280
-// -> 1280: 30 us against 55; 300 x 640 -> 640: 23 against 29; 512 x 1280 -> 1280: 114 against 97).
+// Which kernel: few rows or outputs, the tensor cores where TMA can read the operands, the CUDA cores otherwise.
+// Against the tensor cores (bf16) the row kernel wins up to 8 rows, which read w once (8 x 1280 -> 5120: 8.2 us against 11.4),
+// and up to 32 rows for about 45000 outputs (32 x 512 -> 1000: 3.7 against 5.1; 48 x 1280 -> 1280: 9.3 against 7.5; more
+// rows stay on the tensor cores, where a row's sums do not depend on how many there are).  Against the tiles of the
+// CUDA cores (fp32) it wins while the tiles are few: they take about 0.07 us per column of K whatever their number up to two
+// per SM, and it takes 9e-8 us per product and 3e-5 per output (512 x 640 -> 640: 28 us against 40; 1024 x 640 -> 640: 53 against
+// 50; 8192 x 64 -> 64: 18 against 7).
 cudaError_t launch_matmul(const MatmulArgs& a, int num_sms, cudaStream_t st) {
     const bool tma = matmul_tma_operands(a);
-    if (tma ? a.M <= 8 : a.M <= 16 || (double)a.M * a.N <= 450000.0) return launch_matmul_rows(a, num_sms, st);
+    const double outputs = (double)a.M * a.N, K = (double)a.K0 + a.K1;
+    const bool few = tma ? a.M <= 8 || (a.M <= 32 && outputs <= 45000.0) : a.M <= 16 || outputs * (K + 330.0) <= 780000.0 * K;
+    if (few && a.M <= kMaxRowsM) return launch_matmul_rows(a, num_sms, st);
     return tma ? launch_matmul_tc(a, 0, num_sms, st) : launch_matmul_simt(a, num_sms, st);
 }
 
