@@ -418,8 +418,8 @@ int wino_group_norm(const wino_group_norm_args* args, void* stream);
  * Sums, activation and the residual's addition are fp32 (bf16 products are
  * exact in it); out is rounded once (to nearest even).
  * bf16 operands whose bases and pitches are multiples of 16 bytes (and K of 8
- * when there is an a2) run on the tensor cores; others, and fp32 ones, on the
- * CUDA cores.
+ * when there is an a2) run on the tensor cores unless the rows are few; others,
+ * and fp32 ones, on the CUDA cores.
  * Errors: INVALID_ARG (sizes not positive or above 2^31 - 1025, more than 2^40
  * values in a matrix, pitch, type, alignment, overlap), CUDA.
  */
