@@ -89,6 +89,16 @@ __device__ __forceinline__ void shift_words(uint32_t (&p)[N], int elems) {
     }
 }
 
+// Bytes of a 16-byte unit of values of SIZE bytes of which `values` (one at least) lie before the row's end.  (Clamped
+// before it is multiplied: a row has up to 2^31 values, and their bytes would pass an int.)
+template <int SIZE>
+__host__ __device__ constexpr int unit_bytes(int values) {
+    return (values < 16 / SIZE ? values : 16 / SIZE) * SIZE;
+}
+static_assert(unit_bytes<2>(3) == 6 && unit_bytes<2>((1 << 30) + 1) == 16 && unit_bytes<4>((1 << 29) + 1) == 16 &&
+                  unit_bytes<4>(2147483647) == 16,
+              "a unit has at most 16 bytes however long its row is");
+
 struct Tail {
     uint64_t full[kMaxStages];     // leader: both CTAs' operands of the stage have landed
     uint64_t empty[kMaxStages];    // the pair's MMAs have read the stage
@@ -386,18 +396,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     const int n0 = origin_n(t, c), left = p.m.N - n0, rows = p.m.M - origin_m(t) - 32 * quad, u = lane & 7;
                     const TO* at = res + (size_t)(p.m.M - rows + (lane >> 3)) * p.m.ldr + n0;
                     unsigned char* dst = res_rows + (lane >> 3) * kRowPitch + 16 * u;
+                    const TO* res_end = res + (size_t)(p.m.M - 1) * p.m.ldr + p.m.N;   // (of the debug build's check)
+                    auto copy = [&](unsigned char* to, const TO* from, int values) {   // (zeros behind the row's end)
+                        const int bytes = unit_bytes<(int)sizeof(TO)>(values);
+                        if (in_bounds((size_t)(from - res) + (size_t)bytes / sizeof(TO) - 1, (size_t)(res_end - res), &g_err))
+                            copy_async16(to, from, bytes);
+                    };
 #pragma unroll 2
                     for (int r = lane >> 3; r < min(32, rows); r += 4, at += 4 * p.m.ldr, dst += 4 * kRowPitch) {
                         const int d = E * u - ((int)(reinterpret_cast<uintptr_t>(at) / sizeof(TO)) & (E - 1));
                         if (d < left) {
-                            if (at + d >= res) {   // (zeros behind the row's end)
-                                copy_async16(dst, at + d, min(16, (left - d) * (int)sizeof(TO)));
-                            } else {               // the tensor starts inside the unit
+                            if (at + d >= res) {
+                                copy(dst, at + d, left - d);
+                            } else {   // the tensor starts inside the unit
                                 for (int e = (int)(res - at) - d; e < E && d + e < left; ++e) reinterpret_cast<TO*>(dst)[e] = at[d + e];
                             }
                         }
-                        if (u == 0 && d < 0 && d + 8 * E < left)
-                            copy_async16(dst + 128, at + d + 8 * E, min(16, (left - d - 8 * E) * (int)sizeof(TO)));
+                        if (u == 0 && d < 0 && d + 8 * E < left) copy(dst + 128, at + d + 8 * E, left - d - 8 * E);
                     }
                 }
             }

@@ -395,6 +395,25 @@ def test_matmul_beyond_32_bit_offsets(cuda_dev, M, K, N):
         assert torch.equal(y[lo:lo + part.shape[0]], wino.matmul(part, w))
 
 
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("variant", ["release", "debug"])
+def test_matmul_rows_longer_than_2_gb(cuda_dev, out, variant):
+    """Rows of the output and of the residual of more than 2^31 bytes (each row starts anywhere within 16): columns at both
+    ends and on either side of where as many bytes are left, against 64 bits."""
+    M, K = 9, 8
+    N = (1 << 31) // out.itemsize + 1
+    a, w = randn(1, M, K, dtype=BF16), torch.empty(N, K, device="cuda", dtype=BF16)
+    res = torch.empty(M, N, device="cuda", dtype=out)
+    for r in (*w.split(1 << 27), *res):
+        r.normal_()
+    ranges = [slice(lo, lo + 700) for lo in (0, N // 2 - 350, N - 700)]
+    kept = [res[:, s].clone() for s in ranges]
+    assert wino.matmul(a, w, residual=res, out=res, variant=variant) is res
+    assert wino.check_device_error_ops(variant=variant) == wino.OK
+    for s, r in zip(ranges, kept):
+        check(res[:, s], *ref_matmul(a, w[s], None, "none", r, None, out), "columns from %d" % s.start)
+
+
 def test_matmul_residual_of_infinities(cuda_dev):
     a, w = randn(1, 40, 64, dtype=BF16), randn(2, 48, 64, dtype=BF16)
     res = randn(3, 40, 48, dtype=BF16)
