@@ -66,14 +66,16 @@ Region region(const void* p, size_t rows, size_t cols, int64_t pitch, size_t es)
     return {reinterpret_cast<uintptr_t>(p), rows, cols * es, (size_t)pitch * es};
 }
 // Whether the two share a byte.  Column ranges of one wider buffer (equal pitches) are told apart;
-// otherwise overlapping address ranges count as sharing.
+// otherwise overlapping address ranges count as sharing.  A single row's pitch may be anything, 0 too: it is not looked at.
 bool overlap(const Region& a, const Region& b) {
     if (!a.p || !b.p) return false;
     const uintptr_t ae = a.p + (a.rows - 1) * a.pitch + a.width, be = b.p + (b.rows - 1) * b.pitch + b.width;
     if (ae <= b.p || be <= a.p) return false;
-    if (a.pitch != b.pitch) return true;
-    const size_t d = b.p >= a.p ? (b.p - a.p) % a.pitch : (a.pitch - (a.p - b.p) % a.pitch) % a.pitch;
-    return !(d >= a.width && d + b.width <= a.pitch);
+    if (a.rows == 1 && b.rows == 1) return true;
+    const size_t pitch = a.rows == 1 ? b.pitch : a.pitch;
+    if (b.rows > 1 && b.pitch != pitch) return true;
+    const size_t d = b.p >= a.p ? (b.p - a.p) % pitch : (pitch - (a.p - b.p) % pitch) % pitch;
+    return !(d >= a.width && d + b.width <= pitch);
 }
 // Exactly the same matrix: an operator may update it in place.
 bool same(const Region& a, const Region& b) { return a.p == b.p && a.width == b.width && (a.pitch == b.pitch || a.rows == 1); }

@@ -78,6 +78,25 @@ def test_matmul_refuses(lib, kw):
     assert product(lib, **kw) == wino.ERR_INVALID_ARG
 
 
+def test_pitches_of_single_rows(lib):
+    """A single row's pitch is read by nothing: 0 and any other count as the row's length in the overlap check."""
+    one = dict(N=1, H=1, W=1)
+    for pitch in (0, 1, 64, 128, 200):
+        for at in (2, 126, -126):
+            assert norm(lib, x_pitch=pitch, y_pitch=pitch, y=P[0] + at, **one) == wino.ERR_INVALID_ARG
+        assert product(lib, M=1, N=1, a_pitch=pitch, out_pitch=pitch, residual_pitch=pitch, residual=0, out=P[0] + 2) == wino.ERR_INVALID_ARG
+        assert product(lib, M=1, N=48, out_pitch=pitch, residual_pitch=pitch, residual=P[5] + 2) == wino.ERR_INVALID_ARG
+    # side by side, and the same row: past the overlap check, refused for the channels after it
+    C = wino.GROUP_NORM_MAX_CHANNELS + 32
+    for pitch in (0, 7, C):
+        for y in (P[0] + 2 * C, P[0] - 2 * C, P[0]):
+            assert norm(lib, C=C, x_pitch=pitch, y_pitch=pitch, x=P[0], y=y, add=0, gamma=0, beta=0, **one) == wino.ERR_UNSUPPORTED
+    # a single row between the columns that the output writes, and one that reaches into them
+    wide = dict(C=C, x_pitch=C, y_pitch=4 * C, add=0, beta=0)
+    assert norm(lib, gamma=P[5] + 2 * C, **wide) == norm(lib, gamma=P[5] + 4 * C, **wide) == wino.ERR_UNSUPPORTED
+    assert norm(lib, gamma=P[5] + 2 * C - 4, **wide) == norm(lib, gamma=P[5] + 4 * C + 4, **wide) == wino.ERR_INVALID_ARG
+
+
 def test_null_arguments_are_refused(lib):
     assert lib.wino_group_norm(None, None) == wino.ERR_INVALID_ARG
     assert lib.wino_matmul(None, None) == wino.ERR_INVALID_ARG
