@@ -27,7 +27,7 @@ LIB_DEBUG = os.path.join(HERE, "libwino_b200_debug.so")
 SOURCES = ["plan.cpp", "api.cu", "weight_transform.cu", "input_transform.cu", "hadamard_tc.cu",
            "hadamard_simt.cu", "output_transform.cu", "input_quant.cu", "noalloc.cu", "fused_small.cu",
            "ops_api.cu", "group_norm.cu", "matmul_simt.cu", "matmul_rows.cu", "matmul_tc.cu"]
-HEADERS = ["plan.h", "common.cuh", "sm100.cuh", "kernels.h", "ops.h"]
+HEADERS = ["plan.h", "common.cuh", "sm100.cuh", "kernels.h", "ops.h", "group_norm_split.h"]
 TORCH_OPS = os.path.join(HERE, "torch_ops_b200.so")   # torch marshalling of the operators beside the convolution
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

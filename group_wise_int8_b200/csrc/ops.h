@@ -131,11 +131,7 @@ struct GroupNormArgs {
     bool x_bf16, y_bf16;
 };
 
-// How a call is cut: a cluster of `cluster` CTAs per (image, slab of `gps` groups).
-struct GroupNormSplit {
-    int gps, cluster;
-};
-GroupNormSplit group_norm_split(const GroupNormArgs& a, int vec, int num_sms);
+struct GroupNormSplit;
 // split: null for the rule's choice.
 cudaError_t launch_group_norm(const GroupNormArgs& a, int num_sms, const GroupNormSplit* split, cudaStream_t st);
 

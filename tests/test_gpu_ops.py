@@ -131,6 +131,32 @@ def test_group_norm_matches_64_bits(cuda_dev, name, variant):
     assert wino.check_device_error_ops(variant=variant) == wino.OK
 
 
+NARROW = {
+    # N, H, W, C, groups, dtype: much shared memory beside the kept rows, by hundreds of groups of one or two channels in a slab
+    "one_channel_911": (2, 32, 32, 911, 911, F32),
+    "one_channel_1061": (1, 16, 16, 1061, 1061, F32),
+    "one_channel_2039": (1, 16, 16, 2039, 2039, BF16),
+    "two_channels_907": (2, 32, 32, 1814, 907, BF16),
+    "one_channel_2048": (1, 24, 20, 2048, 2048, BF16),
+    "two_channels_1024": (1, 40, 40, 2048, 1024, F32),
+    "one_channel_1021": (1, 160, 100, 1021, 1021, BF16),
+    "one_channel_16381": (1, 9, 5, 16381, 16381, F32),
+    # clusters of 16 CTAs with an SM each
+    "two_channels_2018": (3, 8, 8, 4036, 2018, F32),
+    "two_channels_523": (3, 16, 16, 1046, 523, BF16),
+    "one_wide_group": (8, 15, 17, 15504, 1, F32),
+}
+
+
+@pytest.mark.parametrize("variant", ["release", "debug"])
+@pytest.mark.parametrize("name", NARROW)
+def test_group_norm_of_many_narrow_groups(cuda_dev, name, variant):
+    N, H, W, C, groups, dtype = NARROW[name]
+    run_norm(randn(1, N, H, W, C, dtype=dtype, mean=0.7), groups, randn(2, C, mean=1.0, spread=0.3), randn(3, C), act="silu",
+             variant=variant)
+    assert wino.check_device_error_ops(variant=variant) == wino.OK
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_group_norm_of_constants_and_far_means(cuda_dev, dtype):
     """A constant group has variance 0; a mean of 1000 spreads keeps its digits (the pivot)."""

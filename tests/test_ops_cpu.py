@@ -97,6 +97,70 @@ def test_pitches_of_single_rows(lib):
     assert norm(lib, gamma=P[5] + 2 * C - 4, **wide) == norm(lib, gamma=P[5] + 4 * C + 4, **wide) == wino.ERR_INVALID_ARG
 
 
+SPLITS = r"""
+#include <cstdio>
+#include "group_norm_split.h"
+using namespace wino;
+using namespace wino::group_norm;
+int main() {
+    long calls = 0;
+    auto fail = [&](const char* what, const GroupNormShape& a, int vec, const GroupNormSplit& s) {
+        std::printf("%s: N %d, HW %ld, C %d, groups %d, %d bytes, vec %d -> %d groups, %d CTAs\n", what, a.N, a.HW, a.C, a.groups,
+                    a.es, vec, s.gps, s.cluster);
+        return 1;
+    };
+    const long pixels[] = {1, 2, 7, 64, 255, 256, 1024, 5000, 65536, 1l << 22, 1l << 30};
+    const int images[] = {1, 2, 3, 8, 40, 3000};
+    for (int groups = 1; groups <= 16384; groups += groups < 40 ? 1 : (groups < 2100 ? 23 : 389))
+        for (int cg = 1; (long)groups * cg <= 16384; cg += cg < 5 ? 1 : cg / 3)
+            for (long HW : pixels)
+                for (int N : images) {
+                    if ((HW + N + groups) % 3 != 0) continue;   // a third of them
+                    for (int form = 0; form < 4; ++form) {
+                        const GroupNormShape a = {HW, N, groups * cg, groups, form & 1 ? 2 : 4};
+                        const int vec = form & 2 ? 16 / a.es : 1;
+                        if (a.C % vec != 0) continue;
+                        ++calls;
+                        const GroupNormSplit s = choose(a, vec, 148);
+                        Split k;
+                        if (make_split(a, vec, s, &k) > kMaxSmem) return fail("too much shared memory", a, vec, s);
+                        if (s.gps * k.slabs != groups || k.nv * vec != s.gps * cg) return fail("no whole slabs", a, vec, s);
+                        if (s.cluster > HW || (s.cluster & (s.cluster - 1)) || s.cluster > kMaxCluster) return fail("no cluster", a, vec, s);
+                        if ((long)k.share * s.cluster + k.extra != HW || k.extra >= s.cluster) return fail("rows lost", a, vec, s);
+                        if (k.res_rows * (long)k.nch * a.es > k.keep_bytes) return fail("kept rows overlap", a, vec, s);
+                        for (int tid = 0; tid < kThreads; ++tid)
+                            if ((int)((uint32_t)tid * k.inv_tv >> 20) != tid / k.TV) return fail("row offsets", a, vec, s);
+                        if (k.inv_cg)
+                            for (int c = k.nch - 1; c >= 0; c -= 1 + k.nch / 7)
+                                if ((int)(((uint64_t)c * k.inv_cg) >> 32) != c / cg) return fail("groups of channels", a, vec, s);
+                    }
+                }
+    std::printf("ok %ld\n", calls);
+    return 0;
+}
+"""
+
+
+def test_every_split_fits(tmp_path):
+    """The group norm's split rule over its whole range (up to 16384 channels in groups of any width): the chosen split's
+    shared memory fits, its slabs and rows are whole."""
+    src, exe = tmp_path / "splits.cpp", tmp_path / "splits"
+    src.write_text(SPLITS)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", os.path.join(ROOT, "group_wise_int8_b200", "csrc"), str(src), "-o", str(exe)],
+                   check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stdout
+    assert int(r.stdout.split()[1]) > 100000
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up: needs a machine on which no launch can follow")
+@pytest.mark.parametrize("N,hw,C,groups", [(2, 1024, 911, 911), (1, 256, 1061, 1061), (1, 256, 2039, 2039), (2, 1024, 1814, 907)])
+def test_narrow_groups_reach_the_launch(lib, N, hw, C, groups):
+    """Their exchange areas outgrow shared memory in the cheapest split; the call takes another one (and then finds no device)."""
+    assert norm(lib, N=N, H=hw, W=1, C=C, groups=groups, x_pitch=C, y_pitch=C, y=1 << 40) == wino.ERR_CUDA
+    assert lib.wino_last_cuda_error(None) != 9   # cudaErrorInvalidConfiguration
+
+
 def test_null_arguments_are_refused(lib):
     assert lib.wino_group_norm(None, None) == wino.ERR_INVALID_ARG
     assert lib.wino_matmul(None, None) == wino.ERR_INVALID_ARG
