@@ -21,7 +21,9 @@
 //
 // Statistics: a thread owns one vector of channels and strides over pixels.
 // Per channel it sums d and d*d with d = x - p, p the first value it sees, so
-// that a mean far from zero costs no digits, and (mean, M2) pairs are joined by
+// that a mean far from zero costs no digits.  Every kBlock rows (more than are kept) the pivot moves to the mean of the
+// rows so far: around a first value far from the rest, thousands of equal squares would be summed, of
+// which M2 is the small difference.  (mean, M2) pairs are joined by
 //   mean = sum n_i mean_i / n,  M2 = sum M2_i + sum n_i (mean_i - mean)^2:
 // a channel's pairs around one of their means, the channels of a group and the CTAs of a cluster (whose
 // means may lie far apart) with the joint mean first.  All of it is fp32; M2 never falls below zero but by rounding.
@@ -40,6 +42,8 @@ namespace {
 using namespace group_norm;
 
 __device__ int g_err;   // first failed index check since group_norm_take_error (debug build)
+
+constexpr int kBlock = 64;   // rows between two recentrings of a thread's sums (more than are ever kept)
 
 // A thread's VEC consecutive values: 16 bytes, or one value where alignment allows no more.
 template <typename T, int VEC>
@@ -70,6 +74,7 @@ struct Vec<T, 1> {
 template <int VEC>
 struct Sums {
     static constexpr int kPairs = VEC / 2;
+    using Part = uint64_t;
     uint64_t p[kPairs], s[kPairs], q[kPairs];
     __device__ __forceinline__ void start(const float (&x)[VEC]) {
 #pragma unroll
@@ -86,6 +91,23 @@ struct Sums {
             q[i] = f2_fma(d, d, q[i]);
         }
     }
+    // Moves the pivot to the mean of the `rows` values so far; their squares go to `whole`.  (The sums follow the
+    // pivot's actual step, so neither its rounding nor 1 / rows needs to be exact.)
+    __device__ __forceinline__ void recentre(float rows, uint64_t (&whole)[kPairs]) {
+        const uint64_t n = f2_pack(-rows, -rows), r = f2_pack(reciprocal(rows), reciprocal(rows));
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const uint64_t to = f2_fma(s[i], r, p[i]), step = f2_sub(to, p[i]), left = f2_fma(n, step, s[i]);
+            whole[i] = f2_add(whole[i], f2_sub(q[i], f2_mul(step, f2_add(s[i], left))));
+            p[i] = to;
+            s[i] = left;
+            q[i] = 0ull;
+        }
+    }
+    __device__ __forceinline__ void join(const uint64_t (&whole)[kPairs]) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) q[i] = f2_add(q[i], whole[i]);
+    }
     __device__ __forceinline__ void get(float (&pv)[VEC], float (&sv)[VEC], float (&qv)[VEC]) const {
 #pragma unroll
         for (int i = 0; i < kPairs; ++i) {
@@ -97,6 +119,8 @@ struct Sums {
 };
 template <>
 struct Sums<1> {
+    static constexpr int kPairs = 1;
+    using Part = float;
     float p, s, q;
     __device__ __forceinline__ void start(const float (&x)[1]) {
         p = x[0];
@@ -107,6 +131,14 @@ struct Sums<1> {
         s += d;
         q = fmaf(d, d, q);
     }
+    __device__ __forceinline__ void recentre(float rows, float (&whole)[kPairs]) {
+        const float to = fmaf(s, reciprocal(rows), p), step = to - p, left = fmaf(-rows, step, s);
+        whole[0] += q - step * (s + left);
+        p = to;
+        s = left;
+        q = 0.0f;
+    }
+    __device__ __forceinline__ void join(const float (&whole)[kPairs]) { q += whole[0]; }
     __device__ __forceinline__ void get(float (&pv)[1], float (&sv)[1], float (&qv)[1]) const {
         pv[0] = p;
         sv[0] = s;
@@ -301,12 +333,23 @@ __global__ void __launch_bounds__(kThreads, 2) group_norm_kernel(const GroupNorm
             V::load(fetch(0), e);
             sums.start(e);
         }
-#pragma unroll 4
-        for (int i = kept; i < mine; ++i) {
+        auto read = [&](int i) {
             const Raw raw = fetch(i);
             if (VEC == 1 && (whole || i < k.res_per)) keep[(tr + i * RP) * nv + v] = raw;
             V::load(raw, e);
             sums.add(e);
+        };
+#pragma unroll 4
+        for (int i = kept; i < min(mine, kBlock); ++i) read(i);
+        if (mine > kBlock) {
+            typename Sums<VEC>::Part squares[Sums<VEC>::kPairs] = {};   // of the rows before the last recentring
+            for (int i = kBlock; i < mine;) {
+                sums.recentre((float)i, squares);
+                const int end = min(i + kBlock, mine);
+#pragma unroll 4
+                for (; i < end; ++i) read(i);
+            }
+            sums.join(squares);
         }
         const float inv = tr < more ? inv1 : inv0;
         float p[VEC], sum[VEC], q[VEC];
