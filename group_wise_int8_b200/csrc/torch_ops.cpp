@@ -11,6 +11,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -73,13 +74,17 @@ int64_t pitch_of(const char* name, const at::Tensor& t) {
     return rows > 1 ? pitch : last;
 }
 
-// These operators have no backward pass: a gradient is refused, not dropped.
+// These operators have no derivatives: a gradient or a forward-mode tangent is refused, not dropped.
 template <typename... T>
 void no_grad(const T*... t) {
-    if (!c10::GradMode::is_enabled()) return;
-    for (const at::Tensor* x : {t...})
-        if (x && x->requires_grad())
+    const bool backward = c10::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    for (const at::Tensor* x : {t...}) {
+        if (!x) continue;
+        if (backward && x->requires_grad())
             refuse("an input requires grad, and this operator has no backward pass: call it under torch.no_grad()");
+        if (forward && x->_fw_grad(/*level=*/0).defined())
+            refuse("an input carries a forward-mode tangent, and this operator has no derivative: unpack the dual tensor first");
+    }
 }
 
 int as_int(PyObject* o, const char* name) {

@@ -635,6 +635,30 @@ def test_two_host_threads(cuda_dev):
     assert not failed
 
 
+def test_forward_mode_tangents_are_refused(cuda_dev):
+    import torch.autograd.forward_ad as fwd
+    x, g, a, w = randn(1, 1, 4, 4, 32), randn(2, 32), randn(3, 4, 32), randn(4, 8, 32)
+    with fwd.dual_level():
+        dual = {k: fwd.make_dual(t, torch.ones_like(t)) for k, t in dict(x=x, g=g, a=a, w=w).items()}
+        for call in (lambda: wino.group_norm(dual["x"], 8), lambda: wino.group_norm(x, 8, gamma=dual["g"]),
+                     lambda: wino.group_norm(x, 8, x2=dual["x"]), lambda: wino.group_norm(x, 8, out=dual["x"]),
+                     lambda: wino.matmul(dual["a"], w), lambda: wino.matmul(a, dual["w"]),
+                     lambda: wino.matmul(a, w, residual=dual["a"][:, :8].contiguous())):
+            for mode in (torch.enable_grad, torch.no_grad):   # (which stops the recording of backward passes only)
+                with mode(), pytest.raises(ValueError, match="tangent"):
+                    call()
+        # their primals, and plain tensors beside them, are fine
+        assert torch.equal(wino.matmul(fwd.unpack_dual(dual["a"]).primal, w), wino.matmul(a, w))
+        with fwd._set_fwd_grad_enabled(False):
+            assert torch.equal(wino.matmul(dual["a"], w), wino.matmul(a, w))
+    with pytest.raises((RuntimeError, ValueError)):
+        torch.func.jvp(lambda t: wino.matmul(t, w), (a,), (a,))
+    with pytest.raises((RuntimeError, ValueError)):
+        torch.func.grad(lambda t: wino.matmul(t, w).sum())(a)
+    with pytest.raises((RuntimeError, ValueError)):
+        torch.func.vmap(lambda t: wino.matmul(t, w))(a[None])
+
+
 def test_binding_refusals(cuda_dev):
     x, a, w = randn(1, 1, 4, 4, 32, dtype=BF16), randn(2, 4, 32, dtype=BF16), randn(3, 8, 32, dtype=BF16)
     for bad in (lambda: wino.group_norm(x[0], 8), lambda: wino.group_norm(x.half(), 8),
