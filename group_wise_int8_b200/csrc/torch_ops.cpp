@@ -74,6 +74,13 @@ int64_t pitch_of(const char* name, const at::Tensor& t) {
     return rows > 1 ? pitch : last;
 }
 
+// A view that torch negates when it is read holds the values' negatives in memory.
+template <typename... T>
+void no_negation(const T*... t) {
+    for (const at::Tensor* x : {t...})
+        if (x && x->is_neg()) refuse("a tensor is a lazily negated view (as the imaginary part of a conjugate is): call resolve_neg() first");
+}
+
 // These operators have no derivatives: a gradient or a forward-mode tangent is refused, not dropped.
 template <typename... T>
 void no_grad(const T*... t) {
@@ -143,6 +150,7 @@ PyObject* group_norm(PyObject*, PyObject* const* o, Py_ssize_t n) {
         if (!x.is_cuda() || x.dim() != 4) refuse("x must be a CUDA tensor [N][H][W][C]");
         const at::ScalarType dtype = x.scalar_type();
         if (code_of(dtype) < 0) refuse(std::string("unsupported dtype ") + c10::toString(dtype));
+        no_negation(&x, x2, add, gamma, beta, given);
         no_grad(&x, x2, add, gamma, beta, given);
         const auto sz = x.sizes();
         wino_group_norm_args g = {};
@@ -200,6 +208,7 @@ PyObject* matmul(PyObject*, PyObject* const* o, Py_ssize_t n) {
         if (!a.is_cuda() || a.dim() < 1 || w.dim() != 2) refuse("a must be a CUDA tensor [...][K] and w [Nout][K + K2]");
         const at::ScalarType dtype = a.scalar_type();
         if (code_of(dtype) < 0) refuse(std::string("unsupported dtype ") + c10::toString(dtype));
+        no_negation(&a, &w, bias, residual, a2, given);
         no_grad(&a, &w, bias, residual, a2, given);
         const auto sz = a.sizes();
         wino_matmul_args g = {};

@@ -659,6 +659,20 @@ def test_forward_mode_tangents_are_refused(cuda_dev):
         torch.func.vmap(lambda t: wino.matmul(t, w))(a[None])
 
 
+def test_negated_views_are_refused(cuda_dev):
+    x, g, a, w = randn(1, 1, 4, 4, 32), randn(2, 32), randn(3, 4, 32), randn(4, 8, 32)
+    neg = torch._neg_view
+    for call in (lambda: wino.group_norm(neg(x), 8), lambda: wino.group_norm(x, 8, gamma=neg(g)), lambda: wino.group_norm(x, 8, x2=neg(x)),
+                 lambda: wino.group_norm(x, 8, out=neg(x)), lambda: wino.matmul(neg(a), w), lambda: wino.matmul(a, neg(w)),
+                 lambda: wino.matmul(a, w, bias=neg(g)[:8]), lambda: wino.matmul(a, w, a2=neg(a))):
+        with pytest.raises(ValueError, match="negated"):
+            call()
+    c = torch.complex(randn(5, 8, 1), randn(6, 8, 1)).conj().imag   # one column: any distance between rows will do
+    with pytest.raises(ValueError, match="negated"):
+        wino.matmul(c, w[:, :1])
+    assert torch.equal(wino.matmul(neg(a).resolve_neg(), w), -wino.matmul(a, w))
+
+
 def test_binding_refusals(cuda_dev):
     x, a, w = randn(1, 1, 4, 4, 32, dtype=BF16), randn(2, 4, 32, dtype=BF16), randn(3, 8, 32, dtype=BF16)
     for bad in (lambda: wino.group_norm(x[0], 8), lambda: wino.group_norm(x.half(), 8),
