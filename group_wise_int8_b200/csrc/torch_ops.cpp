@@ -13,6 +13,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
@@ -129,11 +130,13 @@ PyObject* guarded(F&& f) {
 
 template <typename Args>
 PyObject* run(Status fn, const Args& args, const at::Tensor& out, PyObject* given) {
-    // (a graph that saved the given tensor for its backward pass finds out, as after torch's own in-place calls)
-    if (given != Py_None) out.unsafeGetTensorImpl()->bump_version();
+    TORCH_CHECK(given == Py_None || !out.is_inference() || c10::InferenceMode::is_enabled(),
+                "out is an inference tensor, which may only be written in inference mode");
     const int rc = fn(&args, c10::cuda::getCurrentCUDAStream(out.get_device()).stream());
     if (rc != WINO_OK) return PyLong_FromLong(rc);
     if (given != Py_None) {
+        // (a graph that saved the given tensor for its backward pass finds out, as after torch's own in-place calls)
+        out.unsafeGetTensorImpl()->bump_version();
         Py_INCREF(given);
         return given;
     }

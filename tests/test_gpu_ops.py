@@ -380,6 +380,28 @@ def test_given_outputs_count_as_changed(cuda_dev):
             z.backward()
 
 
+def test_refused_calls_leave_the_output_unchanged(cuda_dev):
+    """A refused call writes nothing, and a backward pass that saved its output tensor is not told of a change."""
+    x = randn(1, 2, 4, 4, 32).requires_grad_()
+    w, g = randn(2, 32, 32), randn(3, 2, 4, 4, 32)
+    for call in (lambda t: wino.group_norm(g, 5, out=t), lambda t: wino.matmul(g, w, act=9, out=t)):
+        h = x * 2.0
+        kept, version = h.detach().clone(), h._version
+        z = (h * h).sum()
+        with torch.no_grad(), pytest.raises(wino.WinoError):
+            call(h)
+        assert h._version == version and torch.equal(h, kept)
+        z.backward()
+    with torch.inference_mode():
+        frozen = torch.zeros_like(g)
+        assert wino.matmul(g, w, out=frozen) is frozen
+    kept = frozen.clone()
+    for call in (lambda: wino.matmul(w, w, out=frozen[0].view(16, 32)[:4]), lambda: wino.group_norm(g, 4, out=frozen)):
+        with pytest.raises((RuntimeError, ValueError)):
+            call()
+    assert torch.equal(frozen, kept)
+
+
 @pytest.mark.parametrize("M,K,N", [(5, 200, 64), (200, 200, 96), (9000, 128, 640), (512, 2560, 320)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_matmul_non_finite_stays_in_its_row_and_column(cuda_dev, M, K, N, bad):
