@@ -122,6 +122,12 @@ PyObject* guarded(F&& f) {
         return f();
     } catch (const std::invalid_argument& e) {
         PyErr_SetString(PyExc_ValueError, e.what());
+    } catch (const c10::OutOfMemoryError& e) {
+        THPObjectPtr torch(PyImport_ImportModule("torch"));
+        THPObjectPtr type(torch ? PyObject_GetAttrString(torch.get(), "OutOfMemoryError") : nullptr);
+        if (type) PyErr_SetString(type.get(), e.what_without_backtrace());
+    } catch (const c10::Error& e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what_without_backtrace());
     } catch (const std::exception& e) {
         PyErr_SetString(PyExc_RuntimeError, e.what());
     }

@@ -365,7 +365,8 @@ def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = Non
     channels after x's without a concatenation; add: fp32 [N][C + C2]; gamma, beta: fp32 [C + C2]; act: ACT_*;
     out_dtype: bf16 or fp32 (default: out's, else x's).  out may be x (in place, when there is no x2).  Runs on x's
     device, on its current stream unless one is given.  Forward only: inputs that require grad are refused while
-    gradients are recorded, and so are dual tensors of forward-mode differentiation.  Raises ValueError for tensors that do not fit, WinoError for what the library refuses."""
+    gradients are recorded, and so are dual tensors of forward-mode differentiation.  Raises ValueError for tensors that do not fit, WinoError for what the library refuses, and
+    torch.OutOfMemoryError where there is no memory for the output."""
     m, debug = _ops.get(variant) or load_torch_ops(variant)
     if stream is None:
         r = m.group_norm(x, groups, gamma, beta, eps, act, add, x2, out, out_dtype, debug)

@@ -695,6 +695,14 @@ def test_negated_views_are_refused(cuda_dev):
     assert torch.equal(wino.matmul(neg(a).resolve_neg(), w), -wino.matmul(a, w))
 
 
+def test_no_memory_for_the_output(cuda_dev):
+    """An output of 2 TB: torch's own error, and the next call works."""
+    a, w = randn(1, 1 << 20, 8, dtype=BF16), randn(2, 1 << 20, 8, dtype=BF16)
+    with pytest.raises(torch.OutOfMemoryError, match="out of memory"):
+        wino.matmul(a, w)
+    run_matmul(a[:300], w[:40])
+
+
 def test_binding_refusals(cuda_dev):
     x, a, w = randn(1, 1, 4, 4, 32, dtype=BF16), randn(2, 4, 32, dtype=BF16), randn(3, 8, 32, dtype=BF16)
     for bad in (lambda: wino.group_norm(x[0], 8), lambda: wino.group_norm(x.half(), 8),
