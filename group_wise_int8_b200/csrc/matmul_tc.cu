@@ -32,7 +32,9 @@
 // over goes in front of the next chunk (an epilogue group takes consecutive chunks for that), and only the
 // ends of a group's part of a row are stored value by value.  Residual units come in by
 // asynchronous copies a chunk ahead and are shifted back.
-// Every mbarrier wait is bounded; on expiry the CTA records the error and leaves.
+// Every mbarrier wait is bounded.  On expiry the warp records the error and raises its CTA's abort flag, every role
+// leaves its loop, in the other CTA too, and the pair waits (with a limit again) for the loads and MMAs under way before it
+// frees its TMEM and returns.
 #include <algorithm>
 #include <type_traits>
 
@@ -56,7 +58,7 @@ constexpr uint32_t kABytes = kARows * kBK * 2;
 constexpr size_t kSmemBudget = 226 * 1024;
 
 struct TcArgs {
-    MatmulArgs m;
+    MatmulArgs m;   // m.force_timeout: before the pair's last tile the MMA issuer waits 1 ms on a barrier nothing completes
     int BN, kb, stages, buffers, tiles_m, tiles_n, steps0, steps1;   // kb: K blocks of 64 per stage (1 or 2)
 };
 
@@ -106,14 +108,18 @@ struct Tail {
     uint64_t acc_empty[2];         // leader: both CTAs' epilogues have read the accumulator
     uint64_t buf_full[2][kMaxBuffers];       // a group's chunk buffer is free to use, its residual (if any) landed
     uint64_t buf_ready[2][kMaxBuffers];      // ... and holds the output chunk: the group's four warps have written it
+    uint64_t done;                   // after an expiry: the pair's MMAs have completed
+    uint64_t never;                  // completed by nobody: the forced expiry waits on it
     alignas(16) float bias[8][64];   // per epilogue warp
     uint32_t tmem_base;
+    uint32_t issued;                 // stages that this CTA's producer has loaded
     int abort_flag;
 };
 
 // Warp-uniform bounded wait: every lane polls, the loop exits for all lanes together.  (The timer is read only once a
 // few polls have failed: reading it costs more than most waits.)
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          unsigned long long limit_ns = kWaitLimitNs) {
     unsigned long long t0 = 0;
     for (uint32_t it = 0;; ++it) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
@@ -121,7 +127,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
             bool stop = *abort_flag != 0;
             if (it == 63u) {
                 t0 = globaltimer();
-            } else if (!stop && globaltimer() - t0 > kWaitLimitNs) {
+            } else if (!stop && globaltimer() - t0 > limit_ns) {
                 stop = true;
                 *abort_flag = 1;
                 atomicCAS(&g_err, 0, kDevErrTimeout);
@@ -240,6 +246,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 mbar_init(&tail->buf_ready[b][i], 4);
             }
         }
+        if (p.m.force_timeout) mbar_init(&tail->never, 1);
         tail->abort_flag = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -259,10 +266,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto origin_n = [&](const Tile& t, int c) { return t.n * p.BN + c * CW; };
     auto half_chunk = [&](int c) { return CW == 64 && c * CW + CW > p.BN; };   // the tile ends in its middle
 
+    bool ok = true;   // no wait of this warp has run out, and none has been called off
     if (warp == 0) {
         // ------------------------------------------------------- TMA producer
         Peek ring_at(tail->empty, 1u);
-        bool ok = true;
+        uint32_t issued = 0;
         const uint32_t full0 = map_rank(&tail->full[0], 0);
         for (Tile t = first; ok && t.valid(p); t.next(p)) {
             const int m0 = origin_m(t), n0 = t.n * p.BN + (int)half * (p.BN / 2);
@@ -286,8 +294,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                             tma_load_2d_pair(dst + j * block_bytes + kABytes, second ? &tmW1 : &tmW0, bar, k, n0);
                         }
                 }
+                ++issued;
             }
         }
+        if (lane == 0) tail->issued = issued;
     } else if (warp == 1) {
         // --------------------------------------------------------- MMA issuer
         if (half == 0) {
@@ -298,10 +308,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int last1 = p.steps1 ? (p.m.K1 - (p.steps1 - 1) * kBK + 15) / 16 : 0;  // last block
             Peek ring_at(tail->full, 0u);
             int it = 0;
-            bool ok = true;
             for (Tile t = first; ok && t.valid(p); t.next(p), ++it) {
                 const int b = it & 1;
-                if (!warp_wait(&tail->acc_empty[b], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag)) break;
+                if (p.m.force_timeout && t.t + t.step >= p.tiles_m * p.tiles_n) ok = warp_wait(&tail->never, 0u, abort_flag, 1000000ull);
+                ok = ok && warp_wait(&tail->acc_empty[b], (uint32_t)((it >> 1) & 1) ^ 1u, abort_flag);
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t d = tmem_base + (uint32_t)b * 256u;
                 for (int s = 0; s < steps; s += p.kb) {
@@ -335,6 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int g = warp - 2;
             unsigned char* ring = chunks + (size_t)g * NB * kChunkBytes;
             Cursor<CW> cur(first, g, p), ahead = cur;
+            int loads = 0;                   // residual chunks asked for: the i-th into buffer i % NB
             auto hand_out = [&](int buf) {   // a free buffer, for the chunk at `ahead`
                 if (!has_res) {
                     mbar_arrive(&tail->buf_full[g][buf]);
@@ -344,6 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tma_load_2d(ring + buf * kChunkBytes, hc ? &tmResHalf : &tmRes, &tail->buf_full[g][buf],
                                 origin_n(ahead.tile, ahead.c), origin_m(ahead.tile));
                     ahead.next(p);
+                    ++loads;
                 }
             };
             if (lane == 0)
@@ -352,7 +365,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             int buf = 0;
             uint32_t phase = 0;
             for (int i = 0; cur.valid(p); cur.next(p), ++i) {
-                if (!warp_wait(&tail->buf_ready[g][buf], phase, abort_flag)) break;
+                ok = warp_wait(&tail->buf_ready[g][buf], phase, abort_flag);
+                if (!ok) break;
                 if (lane == 0) {
                     const int m0 = origin_m(cur.tile);
                     if (m0 < p.m.M)
@@ -367,7 +381,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     phase ^= 1u;
                 }
             }
-            if (lane == 0) bulk_wait_read<0>();
+            if (lane == 0) {
+                bulk_wait_read<0>();
+                if (!ok)   // (otherwise the epilogue has waited for every residual chunk)
+                    for (int i = max(0, loads - NB); i < loads; ++i) mbar_wait_teardown(&tail->buf_full[g][i % NB], (uint32_t)(i / NB) & 1u);
+            }
         }
     } else {
         // ----------------------------------------------------------- epilogue
@@ -378,7 +396,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t release = map_rank(&tail->acc_empty[0], 0);
         int it = 0, buf = 0;
         uint32_t rphase = 0;
-        bool ok = true;
         // DIRECT: the values of a unit; this warp's rows of the output and of the residual
         constexpr int E = 16 / (int)sizeof(TO);
         unsigned char* out_rows = chunks + (size_t)(warp - 4) * kRowsBytes;
@@ -573,7 +590,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int c0 = first_chunk(t), end = end_chunk(t), m0 = origin_m(t);
             const int lo = origin_n(t, c0), hi = min(min(origin_n(t, end), origin_n(t, 0) + p.BN), p.m.N);
             following.next(p);
-            if (!warp_wait(&tail->acc_full[b], (uint32_t)((it >> 1) & 1), abort_flag)) break;
+            ok = warp_wait(&tail->acc_full[b], (uint32_t)((it >> 1) & 1), abort_flag);
+            if (!ok) break;
             tc_fence_after();
             for (int c = c0; ok && c < end; c += kChunkStep) {
                 const bool last = c + kChunkStep >= end;
@@ -599,11 +617,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (DIRECT) copy_wait_all();
     }
 
-    // Every role is done: the MMAs that read either CTA's shared memory have completed (both epilogues waited
-    // for the last accumulator), and no arrival is under way to a CTA that has left.
+    // Every role of both CTAs is done: the MMAs that read either CTA's shared memory have completed (both epilogues
+    // waited for the last accumulator), and no arrival is under way to a CTA that has left.
+    if (!ok && lane == 0) st_cluster_u32(map_rank(&tail->abort_flag, half ^ 1u), 1u);   // (an expiry ends the other CTA's roles, too)
     tc_fence_before();
     __syncthreads();
     cluster_sync();
+    if (__builtin_expect(*abort_flag, 0)) {   // (of both CTAs.)  Not so after an expiry: wait for what is under way
+        if (threadIdx.x == 0) {
+            mbar_init(&tail->done, 1);
+            fence_mbar_init();
+        }
+        __syncthreads();
+        cluster_sync();
+        if (warp == 0 && half == 0 && lane == 0) {
+            // the newest loads of each stage, by whichever CTA got further: a stage that only one of them has loaded
+            // does not complete, and its loads have landed when the limit has passed
+            const uint32_t n = max(tail->issued, ld_cluster_u32(map_rank(&tail->issued, 1))), S = (uint32_t)p.stages;
+            const unsigned long long t0 = globaltimer();
+            for (uint32_t i = n > S ? n - S : 0u; i < n; ++i)
+                while (!mbar_try_wait(&tail->full[i % S], (i / S) & 1u) && globaltimer() - t0 <= kWaitLimitNs) {}
+        } else if (warp == 1) {
+            if (half == 0 && elect_one()) mma_commit_pair(&tail->done, mask);
+            __syncwarp();
+            if (lane == 0) mbar_wait_teardown(&tail->done, 0u);
+        }
+        tc_fence_before();
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);

@@ -147,6 +147,7 @@ struct MatmulArgs {
     int M, N, K0, K1, act;
     bool bf16;             // operand type: bf16 or fp32
     bool out_bf16;
+    bool force_timeout;    // test hook of the tensor-core kernel: one of its bounded waits runs out
 };
 // The CUDA-core kernel: any type, size, pitch and alignment.
 cudaError_t launch_matmul_simt(const MatmulArgs& a, int num_sms, cudaStream_t st);

@@ -179,6 +179,7 @@ int wino_matmul(const wino_matmul_args* g, void* stream) {
     a.act = g->act;
     a.bf16 = g->dtype == WINO_BF16;
     a.out_bf16 = g->out_dtype == WINO_BF16;
+    a.force_timeout = g->reserved == WINO_DEBUG_FORCE_TIMEOUT;
     nvtxRangePushA("wino: matmul");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = launch_matmul(a, sms(), st);

@@ -434,7 +434,8 @@ typedef struct wino_matmul_args {
     int dtype, out_dtype;
     int M, N, K, K2;
     int act; /* WINO_ACT_* */
-    int reserved;
+    int reserved; /* 0.  (A test hook: WINO_DEBUG_FORCE_TIMEOUT lets a bounded wait of the tensor-core
+                   * kernel run out after 1 ms; out is then undefined.) */
 } wino_matmul_args;
 int wino_matmul(const wino_matmul_args* args, void* stream);
 

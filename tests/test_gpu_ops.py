@@ -657,6 +657,32 @@ def test_two_host_threads(cuda_dev):
     assert not failed
 
 
+@pytest.mark.parametrize("M,K,N,out", [(129, 128, 256, BF16), (512, 2560, 1280, BF16), (9000, 320, 640, BF16), (9001, 64, 517, BF16),
+                                       (20000, 1280, 320, F32)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_bounded_wait_expiry_is_reported_and_recoverable(cuda_dev, M, K, N, out, residual):
+    """A wait of the tensor-core kernel that runs out after 1 ms, before each pair's last tile: the kernel returns at once
+    (both CTAs of a pair leave, with loads and products under way), the error is reported once, and the next call is right."""
+    a, w, res = randn(1, M, K, dtype=BF16), randn(2, N, K, dtype=BF16, spread=K ** -0.5), randn(3, M, N, dtype=out)
+    y = torch.empty(M, N, device="cuda", dtype=out)
+    lib = wino.load_library()
+    want = run_matmul(a, w, residual=res if residual else None, out_dtype=out)
+    assert wino.check_device_error_ops() == wino.OK
+    for _ in range(3):
+        args = wino._MATMUL_ARGS.pack(a.data_ptr(), 0, w.data_ptr(), 0, res.data_ptr() if residual else 0, y.data_ptr(), K, 0, K, N, N,
+                                      wino.BF16, wino.BF16 if out == BF16 else wino.F32, M, N, K, 0, wino.ACT_NONE,
+                                      wino.DEBUG_FORCE_TIMEOUT)
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        start.record()
+        assert lib.wino_matmul(args, torch.cuda.current_stream().cuda_stream) == wino.OK
+        end.record()
+        assert wino.check_device_error_ops() == wino.ERR_DEVICE_TIMEOUT
+        assert wino.check_device_error_ops() == wino.OK
+        assert start.elapsed_time(end) < 500
+        assert torch.equal(wino.matmul(a, w, residual=res if residual else None, out_dtype=out), want)
+    assert wino.check_device_error_ops() == wino.OK
+
+
 def test_forward_mode_tangents_are_refused(cuda_dev):
     import torch.autograd.forward_ad as fwd
     x, g, a, w = randn(1, 1, 4, 4, 32), randn(2, 32), randn(3, 4, 32), randn(4, 8, 32)
