@@ -51,3 +51,61 @@ def test_outliers_at_the_first_pixels(cuda_dev, H, W, C, groups, dtype, rows):
     want, tol = ref_norm(x, groups, "none", F32, outliers, outlier, rows)
     assert (tol < 0.01 * (1 + want.abs())).all()
     check(y, want, tol)
+
+
+def banded(seed, N, H, W, C, dtype):
+    """Every channel and every band of rows has a mean and a spread of its own, so that statistics of a subset differ."""
+    x = randn(seed, N, H, W, C)
+    bands = torch.arange(H, device="cuda") * 24 // max(H, 24)
+    x *= torch.exp(0.5 * randn(seed + 1, 24, C)[bands]).view(1, H, 1, C)
+    x += randn(seed + 2, 24, C)[bands].view(1, H, 1, C) + 0.5 * randn(seed + 3, N, 1, 1, C)
+    return x.to(dtype)
+
+
+IMAGES = {
+    # N, H, W, C, groups, dtype, out, act, rows of a thread at most
+    "level_64": (2, 64, 64, 320, 32, BF16, BF16, "silu", 256),
+    "level_64_f32": (2, 64, 64, 320, 32, F32, F32, "silu", 256),
+    "streamed": (1, 160, 150, 128, 1, BF16, BF16, "silu", 1500),
+    "streamed_f32": (1, 131, 97, 128, 2, F32, F32, "none", 800),
+    "decoder": (1, 256, 256, 128, 32, BF16, BF16, "silu", 4096),
+    "decoder_f32": (1, 256, 240, 128, 32, F32, F32, "none", 4096),
+    "odd": (2, 131, 120, 33, 3, BF16, F32, "none", 1000),
+    "wide_images": (3, 256, 256, 1024, 32, BF16, BF16, "silu", 4096),
+}
+
+
+@pytest.mark.parametrize("name", IMAGES)
+def test_statistics_of_many_pixels(cuda_dev, name):
+    N, H, W, C, groups, dtype, out, act, rows = IMAGES[name]
+    x = banded(1, N, H, W, C, dtype)
+    y = wino.group_norm(x, groups, act={"none": wino.ACT_NONE, "silu": wino.ACT_SILU}[act], out_dtype=out)
+    for n in range(N):
+        want, tol = ref_norm(x[n:n + 1], groups, act, out, rows=rows)
+        check(y[n:n + 1], want, tol, "image %d" % n)
+
+
+def test_the_bound_rejects_statistics_of_a_subset(cuda_dev):
+    """The same bound against 64-bit results (on the CPU) whose statistics leave out one CTA's rows, a 64th of the image (where
+    the output is fp32), or whose variance is off by 1 %: each is off at many elements."""
+    for N, H, W, C, groups, dtype, out, act, rows in (IMAGES["level_64"], IMAGES["streamed"], IMAGES["streamed_f32"], IMAGES["odd"]):
+        x = banded(1, N, H, W, C, dtype)[:1].cpu()
+        want, tol = ref_norm(x, groups, act, out, rows=rows)
+        g = x.double().view(1, H * W, groups, C // groups)
+        for lost in (slice(0, H * W // CTAS), slice(H * W // 2, H * W // 2 + H * W // CTAS), slice(H * W - H * W // 64, H * W), None):
+            kept = g
+            # A 64th is lost in bf16's rounding where a group has many channels: the missing rows' mean over 128 channels lies
+            # 128^-1/2 = 0.09 spreads from the group's, which moves the mean by 0.09 / 64 = 0.0014 of them, against a rounding of
+            # up to 2^-8 = 0.004 of the value; their squares, averaged alike, move the variance by as little.
+            if out == BF16 and lost is not None and lost.start == H * W - H * W // 64:
+                continue
+            if lost is not None:
+                keep = torch.ones(H * W, dtype=torch.bool)
+                keep[lost] = False
+                kept = g[:, keep]
+            mean, var = kept.mean(dim=(1, 3), keepdim=True), kept.var(dim=(1, 3), correction=0, keepdim=True)
+            if lost is None:
+                var = var * 1.01
+            wrong = ref_act(((g - mean) / torch.sqrt(var + 1e-5)).view_as(x), act).to(out)
+            off = ((wrong.double() - want).abs() > tol).double().mean().item()
+            assert off > 0.02, (H, W, lost, off)
