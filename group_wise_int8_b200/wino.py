@@ -351,7 +351,8 @@ def _on_stream(stream, f, tensors):
 
 
 def _failed(status: int, what: str, variant: str):
-    return WinoError(status, what, load_library(variant=variant).wino_last_cuda_error(None))
+    # (the thread's last CUDA error may be an earlier call's)
+    return WinoError(status, what, load_library(variant=variant).wino_last_cuda_error(None) if status == ERR_CUDA else 0)
 
 
 def group_norm(x: torch.Tensor, groups: int, gamma: Optional[torch.Tensor] = None,

@@ -161,6 +161,14 @@ def test_narrow_groups_reach_the_launch(lib, N, hw, C, groups):
     assert lib.wino_last_cuda_error(None) != 9   # cudaErrorInvalidConfiguration
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up: needs a machine on which no launch can follow")
+def test_refusals_name_no_earlier_cuda_error(lib):
+    assert norm(lib) == wino.ERR_CUDA and lib.wino_last_cuda_error(None) != 0   # no device here
+    assert "cudaError" in str(wino._failed(wino.ERR_CUDA, "wino_group_norm", "release"))
+    assert norm(lib, groups=5) == wino.ERR_INVALID_ARG
+    assert "cudaError" not in str(wino._failed(wino.ERR_INVALID_ARG, "wino_group_norm", "release"))
+
+
 def test_null_arguments_are_refused(lib):
     assert lib.wino_group_norm(None, None) == wino.ERR_INVALID_ARG
     assert lib.wino_matmul(None, None) == wino.ERR_INVALID_ARG
