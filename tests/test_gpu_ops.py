@@ -683,6 +683,47 @@ def test_bounded_wait_expiry_is_reported_and_recoverable(cuda_dev, M, K, N, out,
     assert wino.check_device_error_ops() == wino.OK
 
 
+@pytest.mark.parametrize("N,hw,C,groups,dtype", [(65536, 1, 32, 4, BF16), (70001, 2, 33, 3, F32), (131072, 1, 8, 8, F32)])
+def test_group_norm_of_more_images_than_a_grid_dimension(cuda_dev, N, hw, C, groups, dtype):
+    run_norm(randn(1, N, hw, 1, C, dtype=dtype, mean=0.3), groups, randn(2, C), randn(3, C), act="silu", add=randn(4, N, C))
+
+
+@pytest.mark.parametrize("M", [524279, 524280, 524281])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_matmul_of_many_rows_and_one_column(cuda_dev, M, dtype):
+    """Around the most rows that the row kernel's grid holds (fp32 takes it for one column of a long K)."""
+    run_matmul(randn(1, M, 700, dtype=dtype), randn(2, 1, 700, dtype=dtype, spread=0.04), randn(3, 1), "silu", randn(4, M, 1, dtype=dtype))
+
+
+def test_the_same_tensor_in_two_places(cuda_dev):
+    x, a = randn(1, 2, 9, 7, 48, dtype=BF16), randn(2, 300, 64, dtype=BF16)
+    run_norm(x, 6, x2=x, act="silu")
+    p = randn(3, 48)
+    run_norm(x, 6, p, p, add=torch.stack([p, p]))
+    run_matmul(a, a)
+    run_matmul(a, torch.cat([a[:80], a[:80]], 1), a2=a, residual=None)
+    sq = randn(4, 64, 64, dtype=BF16)
+    run_matmul(sq, sq, None, "gelu", sq, None)
+
+
+def test_single_rows_of_any_pitch(cuda_dev):
+    """One pixel or row: its pitch is read by nothing, through the C ABI too."""
+    lib, st = wino.load_library(), torch.cuda.current_stream().cuda_stream
+    x, y = randn(1, 1, 1, 1, 64, dtype=BF16), torch.full((80,), 7.0, device="cuda", dtype=BF16)
+    want = wino.group_norm(x, 8).flatten()
+    a, w = randn(2, 1, 64, dtype=BF16), randn(3, 40, 64, dtype=BF16)
+    product = wino.matmul(a, w).flatten()
+    for pitch in (0, 3, 64, 1000):
+        y.fill_(7.0)
+        args = wino._GROUP_NORM_ARGS.pack(x.data_ptr(), 0, 0, 0, 0, y.data_ptr(), pitch, 0, pitch, wino.BF16, wino.BF16, 1, 1, 1, 64, 0, 8, 0,
+                                          1e-5)
+        assert lib.wino_group_norm(args, st) == wino.OK and torch.equal(y[:64], want) and (y[64:] == 7.0).all()
+        y.fill_(7.0)
+        args = wino._MATMUL_ARGS.pack(a.data_ptr(), 0, w.data_ptr(), 0, 0, y.data_ptr(), pitch, 0, 64, 0, pitch, wino.BF16, wino.BF16,
+                                      1, 40, 64, 0, 0, 0)
+        assert lib.wino_matmul(args, st) == wino.OK and torch.equal(y[:40], product) and (y[40:] == 7.0).all()
+
+
 def test_forward_mode_tangents_are_refused(cuda_dev):
     import torch.autograd.forward_ad as fwd
     x, g, a, w = randn(1, 1, 4, 4, 32), randn(2, 32), randn(3, 4, 32), randn(4, 8, 32)
