@@ -121,7 +121,9 @@ inline GroupNormSplit choose(const GroupNormShape& a, int vec, int num_sms) {
             if (c > 8 && ctas > num_sms) cost *= 2.0;   // clusters of 16 leave SMs idle
             cost *= std::max(1.0, ctas / full);
             if (cost >= best_cost) continue;
-            if (make_split(a, vec, {gps, c}, nullptr) > kMaxSmem) continue;   // (the pairs of many narrow groups, too)
+            // Up to kMaxParams channels, the kept rows (90 KiB), table (24 KiB: 384 entries of 8 channels) and parameters
+            // (24 KiB) leave the exchange 11000 pairs.
+            if ((gps * cg > kMaxParams || (c + 1) * gps > 10000) && make_split(a, vec, {gps, c}, nullptr) > kMaxSmem) continue;
             best_cost = cost;
             best = {gps, c};
         }
