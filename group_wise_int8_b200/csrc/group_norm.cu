@@ -549,12 +549,12 @@ bool aligned(const void* p, long ld_bytes, size_t to) {
 
 }  // namespace
 
-cudaError_t launch_group_norm(const GroupNormArgs& a, int num_sms, const GroupNormSplit* split, cudaStream_t st) {
+cudaError_t launch_group_norm(const GroupNormArgs& a, int num_sms, cudaStream_t st) {
     const int C = a.C0 + a.C1, es = a.x_bf16 ? 2 : 4, eo = a.y_bf16 ? 2 : 4, VEC = 16 / es;
     const bool vec = C % VEC == 0 && a.C0 % VEC == 0 && aligned(a.x, a.ld0 * es, 16) &&
                      (a.C1 == 0 || aligned(a.x2, a.ld1 * es, 16));
     const GroupNormShape shape = {a.HW, a.N, C, a.groups, es};
-    const GroupNormSplit s = split ? *split : choose(shape, vec ? VEC : 1, num_sms);
+    const GroupNormSplit s = choose(shape, vec ? VEC : 1, num_sms);
     Split k;
     const size_t smem = make_split(shape, vec ? VEC : 1, s, &k);
     if (smem > kMaxSmem || a.N > 1000000000) return cudaErrorInvalidConfiguration;

@@ -669,15 +669,8 @@ bool map_2d(CUtensorMap* map, bool bf16, const void* base, int cols, int rows, l
                            strides, box, box_cols * es == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-}  // namespace
-
-bool matmul_tma_operands(const MatmulArgs& a) {
-    return a.bf16 && tma_ok(a.a, a.lda, a.M, 2) && tma_ok(a.w, a.ldw, a.N, 2) &&
-           (a.K1 == 0 || (tma_ok(a.a2, a.lda2, a.M, 2) && a.K0 % 8 == 0));
-}
-
 // Operand tensor maps: boxes of 64 columns x 128 rows of a and a2, x w_rows rows of w.
-bool matmul_operand_maps(const MatmulArgs& a, int w_rows, CUtensorMap (&map)[4]) {
+bool operand_maps(const MatmulArgs& a, int w_rows, CUtensorMap (&map)[4]) {
     const void* w1 = static_cast<const __nv_bfloat16*>(a.w) + a.K0;
     if (!map_2d(&map[0], true, a.a, a.K0, a.M, a.lda, kBK, kARows) || !map_2d(&map[2], true, a.w, a.K0, a.N, a.ldw, kBK, w_rows))
         return false;
@@ -695,7 +688,7 @@ bool matmul_operand_maps(const MatmulArgs& a, int w_rows, CUtensorMap (&map)[4])
 // most (19022 x 544 -> 695 takes 68 us in tiles of 64 columns and 48 in tiles of 128; 271 x 512 -> 128 6.5 in tiles of 64 and
 // 5.4 in tiles of 32).  With fewer than 64 rows, many pairs at a time read the same few lines of a, which takes longer
 // (1280 -> 1280 on 40 pairs: 8.7 us for 16 rows, 6.5 for 64; on 20 pairs 6.7 for both).
-int matmul_tc_width(const MatmulArgs& a, int num_sms) {
+int tile_width(const MatmulArgs& a, int num_sms) {
     const long rows = (a.M + 255L) / 256, pairs = num_sms / 2;
     int best = 256;
     double best_cost = 0;
@@ -711,10 +704,17 @@ int matmul_tc_width(const MatmulArgs& a, int num_sms) {
     return best;
 }
 
-cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStream_t st) {
+}  // namespace
+
+bool matmul_tma_operands(const MatmulArgs& a) {
+    return a.bf16 && tma_ok(a.a, a.lda, a.M, 2) && tma_ok(a.w, a.ldw, a.N, 2) &&
+           (a.K1 == 0 || (tma_ok(a.a2, a.lda2, a.M, 2) && a.K0 % 8 == 0));
+}
+
+cudaError_t launch_matmul_tc(const MatmulArgs& m, int num_sms, cudaStream_t st) {
     TcArgs a = {};
     a.m = m;
-    a.BN = bn > 0 ? bn : matmul_tc_width(m, num_sms);
+    a.BN = tile_width(m, num_sms);
     const long tiles_m = (m.M + 255L) / 256, tiles_n = (m.N + (long)a.BN - 1) / a.BN;
     if (tiles_m * tiles_n > 1073741824L) return cudaErrorInvalidConfiguration;
     a.tiles_m = (int)tiles_m;
@@ -725,7 +725,7 @@ cudaError_t launch_matmul_tc(const MatmulArgs& m, int bn, int num_sms, cudaStrea
     // (a TMA store writes whole 16-byte units: a row that ends inside one would have zeros written behind it)
     const bool direct = (size_t)m.N * so % 16 != 0 || !tma_ok(m.out, m.ldo, m.M, so) || (m.res && !tma_ok(m.res, m.ldr, m.M, so));
     CUtensorMap map[4], out, res, out_half, res_half;
-    if (!matmul_operand_maps(m, a.BN / 2, map)) return cudaErrorInvalidValue;
+    if (!operand_maps(m, a.BN / 2, map)) return cudaErrorInvalidValue;
     out = res = out_half = res_half = map[0];
     if (!direct) {
         const int cols = 128 / (int)so;

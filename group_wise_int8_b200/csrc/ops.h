@@ -131,9 +131,7 @@ struct GroupNormArgs {
     bool x_bf16, y_bf16;
 };
 
-struct GroupNormSplit;
-// split: null for the rule's choice.
-cudaError_t launch_group_norm(const GroupNormArgs& a, int num_sms, const GroupNormSplit* split, cudaStream_t st);
+cudaError_t launch_group_norm(const GroupNormArgs& a, int num_sms, cudaStream_t st);
 
 // --------------------------------------------------------- matrix product
 struct MatmulArgs {
@@ -152,16 +150,13 @@ struct MatmulArgs {
 // The CUDA-core kernel: any type, size, pitch and alignment.
 cudaError_t launch_matmul_simt(const MatmulArgs& a, int num_sms, cudaStream_t st);
 
-// For a few rows (at most 65535 blocks of 16): any type, size, pitch and alignment.
+// For a few rows (at most 65535 blocks of 8): any type, size, pitch and alignment.
 constexpr int kMaxRowsM = 8 * 65535;   // rows that the row kernel's grid holds
 cudaError_t launch_matmul_rows(const MatmulArgs& a, int num_sms, cudaStream_t st);
 
-// The tensor-core kernels take bf16 operands that TMA can read (16-byte aligned bases and pitches).
+// The tensor-core kernel takes bf16 operands that TMA can read (16-byte aligned bases and pitches).
 bool matmul_tma_operands(const MatmulArgs& a);
-bool matmul_operand_maps(const MatmulArgs& a, int w_rows, CUtensorMap (&map)[4]);   // a, a2, w for a, w for a2
-// Persistent pair kernel for outputs of many tiles; bn: tile width (a multiple of 32 up to 256), 0: by the rule.
-int matmul_tc_width(const MatmulArgs& a, int num_sms);
-cudaError_t launch_matmul_tc(const MatmulArgs& a, int bn, int num_sms, cudaStream_t st);
+cudaError_t launch_matmul_tc(const MatmulArgs& a, int num_sms, cudaStream_t st);
 
 // Device error words of the kernels above on the current device: the first error recorded since
 // the last call of the function, which clears it (0: none).

@@ -46,7 +46,7 @@ cudaError_t launch_matmul(const MatmulArgs& a, int num_sms, cudaStream_t st) {
     const double outputs = (double)a.M * a.N, K = (double)a.K0 + a.K1;
     const bool few = tma ? a.M <= 8 || (a.M <= 32 && outputs <= 45000.0) : a.M <= 16 || outputs * (K + 330.0) <= 780000.0 * K;
     if (few && a.M <= kMaxRowsM) return launch_matmul_rows(a, num_sms, st);
-    return tma ? launch_matmul_tc(a, 0, num_sms, st) : launch_matmul_simt(a, num_sms, st);
+    return tma ? launch_matmul_tc(a, num_sms, st) : launch_matmul_simt(a, num_sms, st);
 }
 
 bool natural(const void* p, size_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0; }
@@ -135,7 +135,7 @@ int wino_group_norm(const wino_group_norm_args* g, void* stream) {
     a.x_bf16 = g->x_dtype == WINO_BF16;
     a.y_bf16 = g->y_dtype == WINO_BF16;
     nvtxRangePushA("wino: group norm");
-    const cudaError_t e = launch_group_norm(a, sms(), nullptr, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_group_norm(a, sms(), static_cast<cudaStream_t>(stream));
     nvtxRangePop();
     return status(e);
 }

@@ -312,6 +312,7 @@ class Plan:
 
 
 # ------------------------------------------------- operators beside the convolution
+# The header's structs for calls of the C ABI without torch_ops.cpp (which fills them from the header itself)
 _GROUP_NORM_ARGS = struct.Struct("@6P3q2i6iif")   # wino_group_norm_args
 _MATMUL_ARGS = struct.Struct("@6P5q2i4i2i")       # wino_matmul_args
 TORCH_OPS_PATH = os.path.join(HERE, "torch_ops_b200.so")
