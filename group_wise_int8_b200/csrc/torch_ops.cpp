@@ -75,22 +75,17 @@ int64_t pitch_of(const char* name, const at::Tensor& t) {
     return rows > 1 ? pitch : last;
 }
 
-// A view that torch negates when it is read holds the values' negatives in memory.
+// What torch keeps beside a tensor's memory and these operators do not look at is refused, not dropped: the sign of a
+// lazily negated view, and gradients and forward-mode tangents (the operators have no derivatives).
 template <typename... T>
-void no_negation(const T*... t) {
-    for (const at::Tensor* x : {t...})
-        if (x && x->is_neg()) refuse("a tensor is a lazily negated view (as the imaginary part of a conjugate is): call resolve_neg() first");
-}
-
-// These operators have no derivatives: a gradient or a forward-mode tangent is refused, not dropped.
-template <typename... T>
-void no_grad(const T*... t) {
-    const bool backward = c10::GradMode::is_enabled(), forward = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+void plain(const T*... t) {
     for (const at::Tensor* x : {t...}) {
         if (!x) continue;
-        if (backward && x->requires_grad())
+        if (x->is_neg()) refuse("a tensor is a lazily negated view (as the imaginary part of a conjugate is): call resolve_neg() first");
+        if (!x->unsafeGetTensorImpl()->autograd_meta()) continue;   // (most tensors: the rest takes library calls)
+        if (c10::GradMode::is_enabled() && x->requires_grad())
             refuse("an input requires grad, and this operator has no backward pass: call it under torch.no_grad()");
-        if (forward && x->_fw_grad(/*level=*/0).defined())
+        if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && x->_fw_grad(/*level=*/0).defined())
             refuse("an input carries a forward-mode tangent, and this operator has no derivative: unpack the dual tensor first");
     }
 }
@@ -159,8 +154,7 @@ PyObject* group_norm(PyObject*, PyObject* const* o, Py_ssize_t n) {
         if (!x.is_cuda() || x.dim() != 4) refuse("x must be a CUDA tensor [N][H][W][C]");
         const at::ScalarType dtype = x.scalar_type();
         if (code_of(dtype) < 0) refuse(std::string("unsupported dtype ") + c10::toString(dtype));
-        no_negation(&x, x2, add, gamma, beta, given);
-        no_grad(&x, x2, add, gamma, beta, given);
+        plain(&x, x2, add, gamma, beta, given);
         const auto sz = x.sizes();
         wino_group_norm_args g = {};
         int64_t C = sz[3];
@@ -217,8 +211,7 @@ PyObject* matmul(PyObject*, PyObject* const* o, Py_ssize_t n) {
         if (!a.is_cuda() || a.dim() < 1 || w.dim() != 2) refuse("a must be a CUDA tensor [...][K] and w [Nout][K + K2]");
         const at::ScalarType dtype = a.scalar_type();
         if (code_of(dtype) < 0) refuse(std::string("unsupported dtype ") + c10::toString(dtype));
-        no_negation(&a, &w, bias, residual, a2, given);
-        no_grad(&a, &w, bias, residual, a2, given);
+        plain(&a, &w, bias, residual, a2, given);
         const auto sz = a.sizes();
         wino_matmul_args g = {};
         const int64_t K = sz[sz.size() - 1], Nout = w.size(0);
