@@ -6,9 +6,10 @@
 // skip tensor), which are never joined in memory; a group may straddle them.
 //
 // Bound: device memory (x read once, y written once); per value about 10 fp32
-// operations and, with SiLU, 1.25 special-function operations.  As built, instruction issue in the two row loops (19
-// instructions per value) and the joins between them come first: 8 x 64 x 64 x 320 bf16 with SiLU takes 16.3 us where its
-// 42 MB take 6.4 at the copy rate; 8 x 64 x 64 x 960 48.6 (19.2); 2 x 32 x 32 x 640 fp32 6.2 (1.6).
+// operations and, with SiLU, 1.25 special-function operations.  As built, 8 x 64 x 64 x 320 bf16 with SiLU takes 14.9 us
+// where its 42 MB take 6.4 at the copy rate: 8.5 us of issue slots on the 128 SMs that the split uses (26 instructions
+// per value, 19 of them in the two row loops), and as much again of latency between the phases, in which the schedulers
+// issue nothing half of the time.  8 x 64 x 64 x 960 48.8 (19.2); 2 x 32 x 32 x 640 fp32 6.1 (1.6).
 //
 // Split: an image's channels are cut into slabs of whole groups, and a
 // thread-block cluster of up to 16 CTAs takes one (image, slab), each CTA a

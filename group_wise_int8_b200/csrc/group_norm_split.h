@@ -24,7 +24,7 @@ constexpr int kThreads = 256;          // two CTAs per SM, with registers for a 
 constexpr int kMaxCluster = 16;
 constexpr int kMaxParams = 2048;       // channels whose parameters fit in shared memory
 constexpr int kResBytes = 90 * 1024;   // a CTA's share of the input kept in shared memory
-constexpr size_t kMaxSmem = 227 * 1024;  // of a CTA
+constexpr size_t kMaxSmem = 227 * 1024;   // of a CTA
 
 // What the kernel needs to know of its split, worked out once on the host.  A row offset is a thread's first row
 // within its CTA's pixels; it takes every RP-th row from there.  Index 1 of a pair: the first `extra` CTAs of a
@@ -99,8 +99,8 @@ inline size_t make_split(const GroupNormShape& a, int vec, const GroupNormSplit&
 // The split with the least estimated time, in us: rounds of two CTAs per SM, each a fixed part (launch, joins, exchange)
 // plus its share of the input.  The constants are a fit to every split of 75 shapes (8 x 8 to 256 x 256 pixels, 32 to 2560
 // channels, batches of 1 to 16): its choice took 0.9 % more time than the best split on average and 6 % at most.  8 x 64 x 64 x 320
-// bf16 with SiLU, for one, takes 16.4 in clusters of 8 CTAs of 82 KiB, 17.3 in clusters of 4 of as many bytes (rows of 80
-// bytes, not 160) and 21.0 as 512 CTAs of 41 KiB; 8 x 32 x 32 x 640 takes 9.6 in clusters of 4 and 10.2 in clusters of 8.
+// bf16 with SiLU, for one, took 16.4 there in clusters of 8 CTAs of 82 KiB, 17.3 in clusters of 4 of as many bytes (rows of
+// 80 bytes, not 160) and 21.0 as 512 CTAs of 41 KiB; 8 x 32 x 32 x 640 took 9.6 in clusters of 4 and 10.2 in clusters of 8.
 inline GroupNormSplit choose(const GroupNormShape& a, int vec, int num_sms) {
     const int cg = a.C / a.groups, es = a.es;
     const int unit = vec / gcd(cg, vec);   // groups of the narrowest slab of whole vectors

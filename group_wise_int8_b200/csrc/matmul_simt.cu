@@ -2,8 +2,8 @@
 // type, size, pitch and alignment (fp32 operands, and bf16 ones that TMA cannot
 // read).
 //
-// Bound: the fp32 pipes, 2 M N K operations at 74 TFLOP/s.  8192 x 1280 -> 1280 runs at 43, and fewer tiles than SMs
-// at less (512 x 1280 -> 1280: 17).
+// Bound: the fp32 pipes, 2 M N K operations at 74 TFLOP/s.  8192 x 1280 -> 1280 runs at 44 (the installed library: 58), and fewer tiles than SMs
+// at less (512 x 1280 -> 1280: 17; the library 31).
 //
 // A 128 x 128 or 64 x 64 tile of the output per CTA of 256 threads, 8 x 8 or 4 x 4
 // outputs per thread.  16 columns of K at a time go through shared memory, transposed so that a

@@ -1,10 +1,11 @@
 // Matrix product with bias, activation and residual on the sm_100a tensor cores,
 // for outputs of many tiles: out = act([a | a2] w^T + bias) + residual in bf16
-// operands and fp32 sums.
+// operands and fp32 sums.  (The tensor cores truncate a partial sum where fp32 arithmetic rounds it, once every 16
+// columns of K: up to about K 2^-28 of the terms' magnitudes, 1.9e-5 measured for 5120 terms of one sign.)
 //
 // Bound: the tensor cores when K is long, device memory (activations in, residual
-// in, output out) for the 1x1 convolutions of an image network.  8192 x 1280 -> 5120 with GELU takes 86 us, 1240 TFLOP/s;
-// 32768 x 960 -> 320 with residual 26.7 us where its 106 MB take 16.1 at the copy rate (the operands' way from L2 into the
+// in, output out) for the 1x1 convolutions of an image network.  8192 x 1280 -> 5120 with GELU takes 83 us, 1290 TFLOP/s;
+// 32768 x 960 -> 320 with residual 26.3 us where its 106 MB take 16.1 at the copy rate (the operands' way from L2 into the
 // SMs comes first: 205 MB); 32768 x 320 -> 1280 30 us.
 //
 // Kernel structure (persistent; a cluster of two CTAs, one pair per two SMs, walks
